@@ -412,6 +412,89 @@ int moe_combine(const uint16_t* o, const float* w,
                 const uint16_t* h_s, const uint16_t* ws_down, const float* s,
                 int T, int H, int k, int I_s, uint16_t* y, void* stream);
 
+/*
+ * Operators around the layer, for a model that runs it: the norms between two blocks, rows in 8-bit
+ * integers, and products of them, dense or grouped by expert.  The conventions above hold; sizes are
+ * freer than the layer's.  A call is one launch and takes no workspace, so calls on different streams
+ * or in different captured graphs share nothing.  Inference only, as the layer: none has a gradient.
+ *
+ * Types of residual streams and of product outputs.
+ */
+#define MOE_BF16 0
+#define MOE_F32 1
+
+/*
+ * The boundary of a block: the norm behind it, its gate, the residual add and the norm before the
+ * next block, in one pass over the rows:
+ *     z  = w_post ? norm(y, w_post) : y
+ *     r' = r_scale * r + y_scale * gate * z          (y NULL: r' = r_scale * r)
+ *     u  = norm(r', w_pre)                           (of the fp32 r', before any rounding)
+ *     norm(v, w) = v / sqrt(mean(v^2) + eps) * (w + w_add)
+ * in fp32, each output rounded once.  w_add is 0, or 1 for weights stored around zero.
+ *   r       [T,H] bf16 or fp32 (r_type MOE_BF16, MOE_F32); r_out likewise
+ *   y       [T,H] bf16, the block's output, or NULL (the first boundary)
+ *   w_post  [H] bf16 or NULL: no norm behind the block
+ *   gate    bf16 [H] (gate_rows 1) or [T,H] (gate_rows T), or NULL: 1
+ *   r_out   [T,H] r', or NULL; may be r itself
+ *   w_pre   [H] bf16, given if and only if x or q is
+ *   x       [T,H] bf16 u, or NULL; may be y itself
+ *   q, q_scale  [T,H] int8 and [T] fp32: u quantised as by moe_quantize_i8, or both NULL
+ * H % 16 == 0, 16 <= H <= 16384; T <= 2^24; eps >= 0.
+ */
+int moe_block_norm(const void* r, int r_type, const uint16_t* y, const uint16_t* w_post, const uint16_t* gate,
+                   int gate_rows, float r_scale, float y_scale, const uint16_t* w_pre, float w_add, float eps,
+                   int T, int H, void* r_out, uint16_t* x, int8_t* q, float* q_scale, void* stream);
+
+/*
+ * Rows as 8-bit integers with one scale per row (a token's activations, a weight matrix's output
+ * channels):  scale[r] = max(max_k |x[r,k]|, 2^-100) / 127,  q[r,k] = x[r,k] / scale[r] rounded to nearest
+ * even (computed as x * (127 / max) in fp32), so |q| <= 127.  A row that holds an infinity or a NaN gets
+ * scale NaN and codes 0: products with it are NaN, other rows are not touched by it.
+ *   x [R,K] bf16, q [R,K] int8, scale [R] fp32.  K % 16 == 0, 16 <= K <= 32768; R <= 2^28.
+ */
+int moe_quantize_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, void* stream);
+
+/*
+ * SwiGLU of a gate/up product, quantised for the down product:  h = silu(gu[r,i]) * gu[r,I+i] in fp32,
+ * then as moe_quantize_i8; row_gate [R] fp32 (NULL: 1) multiplies the row's scale (a token's gate on the
+ * shared expert, for example).
+ *   gu [R,2*I] bf16 (gate columns, then up columns), q [R,I] int8, scale [R] fp32.  I as K above.
+ */
+int moe_swiglu_i8(const uint16_t* gu, const float* row_gate, int R, int I, int8_t* q, float* scale, void* stream);
+
+/*
+ * Matrix product in 8-bit integers with a scale per token and per channel:
+ *     c[m,n] = (sum_k a[m,k] b[n,k]) * a_scale[m] * b_scale[n] + bias[n] + add[m,n]
+ * The sum is exact (int32); the rest is fp32, rounded once.
+ *   a [M,K], b [N,K] int8 (every code, -128 included), a_scale [M], b_scale [N] fp32, bias [N] fp32 or NULL,
+ *   add [M,N] bf16 or NULL (may be c itself when c is bf16), c [M,N] bf16 or fp32 (c_type).
+ *   K % 16 == 0, 16 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^20; M <= 2^28.  M = 0 is a successful no-op.
+ */
+int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const float* bias,
+                const uint16_t* add, int M, int N, int K, void* c, int c_type, void* stream);
+
+/*
+ * Products grouped by expert over ragged row counts:
+ *     c[id,:] = a[id / a_div,:] . b[e]^T      for every position p of expert e, id = rows[p]
+ * Expert e owns positions off[e] .. off[e] + n_e - 1 with n_e = counts[e] (counts NULL: off[e+1] - off[e]);
+ * rows NULL: id = p.  Ids outside [0, R) are padding.  Rows of c that no position names are left as they
+ * were; an expert may own no position; no two positions name one row.  off, counts, rows are read on the
+ * device, and positions outside [0, P) are not touched.
+ *   moe_align's outputs serve as they are: off = pad_off, counts, rows = sorted, P = moe_align_max_rows,
+ *   R = T*k; a_div = k reads token rows (gate/up), a_div = 1 assignment rows (down).
+ *   a [(R-1)/a_div + 1, K], b [E,N,K], c [R,N] bf16 or fp32 (c_type); off [E+1], counts [E], rows [P] int32.
+ *   moe_grouped_gemm: a, b bf16, fp32 sums, K % 8 == 0.
+ *   moe_grouped_gemm_i8: a, b int8, int32 sums, times a_scale [rows of a] and b_scale [E,N] as moe_gemm_i8;
+ *   K % 16 == 0.
+ *   1 <= E <= 256; K <= 65536; N % 8 == 0, 8 <= N <= 2^20; P, R <= 2^28 (0: no-op); a_div >= 1.
+ */
+int moe_grouped_gemm(const uint16_t* a, const uint16_t* b, const int32_t* off, const int32_t* counts,
+                     const int32_t* rows, int a_div, int P, int R, int E, int N, int K, void* c, int c_type,
+                     void* stream);
+int moe_grouped_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
+                        const int32_t* off, const int32_t* counts, const int32_t* rows, int a_div, int P, int R,
+                        int E, int N, int K, void* c, int c_type, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,10 @@ EXPORTS = (
     "moe_align", "moe_grouped_gate_up", "moe_grouped_down", "moe_combine", "moe_forward_fp8", "moe_e4m3_to_f32", "moe_forward_q4",
     "moe_bucket_plan", "moe_prefill_runner_create", "moe_prefill_runner_create_fp8", "moe_prefill_runner_run", "moe_prefill_runner_destroy",
     "moe_forward_noalloc", "moe_workspace_sections",
+    "moe_block_norm", "moe_quantize_i8", "moe_swiglu_i8", "moe_gemm_i8", "moe_grouped_gemm", "moe_grouped_gemm_i8",
 )
+BF16 = 0  # MOE_BF16, MOE_F32: types of a residual stream and of a product's output
+F32 = 1
 NOALLOC_WS_BYTES = 64 << 20  # MOE_NOALLOC_WS_BYTES: the fixed workspace of moe_forward_noalloc
 
 
@@ -52,7 +55,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with `python -m sparse_moe_layer_03_amd.build`")
         L = C.CDLL(LIB_PATH)
-        p, i, z, i64 = C.c_void_p, C.c_int, C.c_size_t, C.c_int64
+        p, i, z, i64, f = C.c_void_p, C.c_int, C.c_size_t, C.c_int64, C.c_float
         sig = {
             "moe_status_str": ([i], C.c_char_p),
             "moe_last_error": ([], C.c_char_p),
@@ -82,11 +85,17 @@ def lib():
             "moe_prefill_runner_create_fp8": ([p] * 15 + [i] * 5 + [p, i, p], i),
             "moe_prefill_runner_run": ([p, p, i, p, p], i),
             "moe_prefill_runner_destroy": ([p], i),
+            "moe_block_norm": ([p, i, p, p, p, i, f, f, p, f, f, i, i, p, p, p, p, p], i),
+            "moe_quantize_i8": ([p, i, i, p, p, p], i),
+            "moe_swiglu_i8": ([p, p, i, i, p, p, p], i),
+            "moe_gemm_i8": ([p] * 6 + [i] * 3 + [p, i, p], i),
+            "moe_grouped_gemm": ([p] * 5 + [i] * 6 + [p, i, p], i),
+            "moe_grouped_gemm_i8": ([p] * 7 + [i] * 6 + [p, i, p], i),
         }
         for name, (args, res) in sig.items():
-            f = getattr(L, name)
-            f.argtypes = args
-            f.restype = res
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = res
         _lib = L
     return _lib
 
@@ -288,3 +297,118 @@ def moe_grouped_down(h, w_down, sorted_rows, tiles, n_tiles, T, H, E, k, I, o, s
 def moe_combine(o, w, h_s, ws_down, s, T, H, k, I_s, y, stream=None):
     _check(lib().moe_combine(_p(o), _p(w), _p(h_s), _p(ws_down), _p(s), T, H, k, I_s, _p(y),
                              _stream(stream)))
+
+
+# ------------------------------------------------------------- operators around the layer
+def _need(name, t, dtypes, numel):
+    """Refuses a tensor the C ABI cannot tell from the right one: wrong type, too few elements, strided, or on
+    another device than the current one (whose stream the call is enqueued on).  None passes (the C ABI knows
+    which pointers it requires)."""
+    if t is None or isinstance(t, int):
+        return
+    import torch
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(str(d) for d in dtypes)}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements; {numel} needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+
+
+def _type(name, t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise ValueError(f"{name} is {t.dtype}; expected torch.bfloat16 or torch.float32")
+
+
+def moe_block_norm(r, y, w_post, gate, w_pre, T, H, r_out, x, q, q_scale, r_scale: float = 1.0, y_scale: float = 1.0,
+                   w_add: float = 0.0, eps: float = 1e-6, stream=None):
+    """The type of r (bf16 or fp32) is that of r_out; gate has H elements (one row for all tokens) or T * H."""
+    import torch
+    bf, n = (torch.bfloat16,), T * H
+    r_type = _type("r", r)
+    _need("r", r, (r.dtype,), n)
+    _need("y", y, bf, n)
+    _need("w_post", w_post, bf, H)
+    _need("w_pre", w_pre, bf, H)
+    _need("r_out", r_out, (r.dtype,), n)
+    _need("x", x, bf, n)
+    _need("q", q, (torch.int8,), n)
+    _need("q_scale", q_scale, (torch.float32,), T)
+    gate_rows = 1
+    if gate is not None:
+        gate_rows = 1 if gate.numel() == H else T
+        _need("gate", gate, bf, gate_rows * H)
+    _check(lib().moe_block_norm(_p(r), r_type, _p(y), _p(w_post), _p(gate), gate_rows, r_scale, y_scale, _p(w_pre),
+                                w_add, eps, T, H, _p(r_out), _p(x), _p(q), _p(q_scale), _stream(stream)))
+
+
+def moe_quantize_i8(x, R, K, q, scale, stream=None):
+    import torch
+    _need("x", x, (torch.bfloat16,), R * K)
+    _need("q", q, (torch.int8,), R * K)
+    _need("scale", scale, (torch.float32,), R)
+    _check(lib().moe_quantize_i8(_p(x), R, K, _p(q), _p(scale), _stream(stream)))
+
+
+def moe_swiglu_i8(gu, row_gate, R, I, q, scale, stream=None):
+    import torch
+    _need("gu", gu, (torch.bfloat16,), 2 * R * I)
+    _need("row_gate", row_gate, (torch.float32,), R)
+    _need("q", q, (torch.int8,), R * I)
+    _need("scale", scale, (torch.float32,), R)
+    _check(lib().moe_swiglu_i8(_p(gu), _p(row_gate), R, I, _p(q), _p(scale), _stream(stream)))
+
+
+def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
+    """The type of c (bf16 or fp32) is the output's."""
+    import torch
+    i8, f32 = (torch.int8,), (torch.float32,)
+    c_type = _type("c", c)
+    _need("a", a, i8, M * K)
+    _need("a_scale", a_scale, f32, M)
+    _need("b", b, i8, N * K)
+    _need("b_scale", b_scale, f32, N)
+    _need("bias", bias, f32, N)
+    _need("add", add, (torch.bfloat16,), M * N)
+    _need("c", c, (c.dtype,), M * N)
+    _check(lib().moe_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(bias), _p(add), M, N, K, _p(c), c_type,
+                             _stream(stream)))
+
+
+def _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, dtype):
+    import torch
+    i32 = (torch.int32,)
+    a_rows = (R - 1) // a_div + 1 if R > 0 and a_div > 0 else 0
+    _need("a", a, dtype, a_rows * K)
+    _need("b", b, dtype, E * N * K)
+    _need("off", off, i32, E + 1)
+    _need("counts", counts, i32, E)
+    _need("rows", rows, i32, P)
+    _need("c", c, (c.dtype,), R * N)
+    return a_rows
+
+
+def moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, stream=None):
+    """The type of c (bf16 or fp32) is the output's."""
+    import torch
+    c_type = _type("c", c)
+    _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, (torch.bfloat16,))
+    _check(lib().moe_grouped_gemm(_p(a), _p(b), _p(off), _p(counts), _p(rows), a_div, P, R, E, N, K, _p(c), c_type,
+                                  _stream(stream)))
+
+
+def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, stream=None):
+    """The type of c (bf16 or fp32) is the output's."""
+    import torch
+    c_type = _type("c", c)
+    a_rows = _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, (torch.int8,))
+    _need("a_scale", a_scale, (torch.float32,), a_rows)
+    _need("b_scale", b_scale, (torch.float32,), E * N)
+    _check(lib().moe_grouped_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(off), _p(counts), _p(rows), a_div, P,
+                                     R, E, N, K, _p(c), c_type, _stream(stream)))
