@@ -54,6 +54,8 @@ struct ProductArgs {
   const int32_t* counts;  // [E] positions of each expert, NULL: off[e + 1] - off[e]
   const int32_t* rows;    // [P] output row of each position, NULL: the position itself
   int a_div;              // A row = output row / a_div
+  unsigned div_mul;       // the same division as a multiplication (set by launch_product)
+  int div_shift;
   int P;                  // positions
   int R;                  // output rows; others are skipped
   int E, N;

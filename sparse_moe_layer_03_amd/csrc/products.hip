@@ -8,6 +8,8 @@
 //
 // Grouped: expert e owns positions off[e] .. off[e] + count(e) - 1.  Position p is output row id = rows[p] (or p)
 // and reads A row id / a_div; ids outside [0, R) are padding and are skipped.
+#include <atomic>
+
 #include "block_internal.h"
 
 namespace moe {
@@ -34,6 +36,8 @@ __device__ __forceinline__ i32x16 mma32(const u32x4& b, const u32x4& a, const i3
                                                0);
 }
 
+__device__ const u32x4 kZeros[1] = {{0u, 0u, 0u, 0u}};  // source of the chunks behind a row's end
+
 // Positions of expert e, kept inside [0, P).
 __device__ __forceinline__ void expert_range(const ProductArgs& p, int e, int& first, int& count) {
   const int lo = min(max(p.off[e], 0), p.P);
@@ -48,123 +52,521 @@ __device__ __forceinline__ int output_row(const ProductArgs& p, int pos) {
   return (unsigned)id < (unsigned)p.R ? id : -1;
 }
 
-// Tile `idx` of the list of all experts' BM-row tiles in expert order: (expert, first position, rows), or rows = 0
-// past the end.  Thread e < E counts expert e's tiles; `s` is LDS of 260 ints.
-template <int BM>
-__device__ __forceinline__ void find_tile(const ProductArgs& p, int idx, int* s, int& expert, int& first, int& rows) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  int lo = 0, n = 0;
-  if (tid < p.E) expert_range(p, tid, lo, n);
-  const int tiles = (n + BM - 1) / BM;
-  int incl = tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (tid < 256 && lane == 63) s[tid >> 6] = incl;
-  if (tid == 0) s[6] = 0;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < (tid >> 6) && w < 4; ++w) before += s[w];
-  const int excl = before + incl - tiles;
-  if (tid < p.E && idx >= excl && idx < excl + tiles) {
-    s[4] = tid;
-    s[5] = lo + (idx - excl) * BM;
-    s[6] = min(BM, n - (idx - excl) * BM);
-  }
-  __syncthreads();
-  expert = s[4];
-  first = s[5];
-  rows = s[6];
+// A row of an output row: id / a_div by a multiplication (exact for id < 2^31; div_mul 0: a_div is 1).
+__device__ __forceinline__ int a_row(const ProductArgs& p, int id) {
+  return p.div_mul ? (int)(__umulhi((unsigned)id, p.div_mul) >> p.div_shift) : id;
 }
 
-__device__ __forceinline__ int swz8(int row, int chunk) { return chunk ^ (((row >> 1) ^ ((row & 1) << 2)) & 7); }
-
-// Four consecutive columns of one output row.
-template <bool I8, class A>
-__device__ __forceinline__ void store4(const ProductArgs& p, int id, int expert, int n, const A& acc, int q0) {
-  float v[4];
-  if constexpr (I8) {
-    const float sa = p.a_scale[id / p.a_div];
-    const float4 sb = *reinterpret_cast<const float4*>(p.b_scale + (size_t)expert * p.N + n);
-    const float f[4] = {sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)acc[q0 + i] * sa * f[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = acc[q0 + i];
-  }
-  if (p.bias) {
-    const float4 b = *reinterpret_cast<const float4*>(p.bias + n);
-    v[0] += b.x, v[1] += b.y, v[2] += b.z, v[3] += b.w;
-  }
-  const size_t at = (size_t)id * p.N + n;
-  if (p.add) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p.add + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += bf16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-  }
-  if (p.c_f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) = make_float4(v[0], v[1], v[2], v[3]);
-  else
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.c) + at) = u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
-}
-
-// 64 x 64 tile per workgroup, four waves of 32 x 32, both operands through one LDS stage of 128-byte rows.
-template <bool I8>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
-  __shared__ u32x4 sa[64 * 8], sb[64 * 8];
-  __shared__ int s_tile[8], s_row[64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int expert = 0, first = blockIdx.x * 64, rows = min(64, p.P - first);
-  if (p.off) find_tile<64>(p, blockIdx.x, s_tile, expert, first, rows);
-  if (rows <= 0) return;
-  if (tid < 64) s_row[tid] = tid < rows ? output_row(p, first + tid) : -1;
-  __syncthreads();
-  const int n0 = blockIdx.y * 64;
-  const int wm = wave >> 1, wn = wave & 1;
-  typename Acc<I8>::t32 acc = {};
-  for (int kb = 0; kb < p.Kb; kb += 128) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = i * 32 + tid / 8, c = tid % 8, k = kb + c * 16;
-      const int id = s_row[r];
-      u32x4 va = {0u, 0u, 0u, 0u}, vb = {0u, 0u, 0u, 0u};
-      if (id >= 0 && k < p.Kb)
-        va = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.a) + (size_t)(id / p.a_div) * p.Kb + k);
-      if (n0 + r < p.N && k < p.Kb)
-        vb = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.b) + ((size_t)expert * p.N + n0 + r) * p.Kb + k);
-      sa[r * 8 + swz8(r, c)] = va;
-      sb[r * 8 + swz8(r, c)] = vb;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int c = 2 * s + (lane >> 5), ra = wm * 32 + (lane & 31), rb = wn * 32 + (lane & 31);
-      acc = mma32(sb[rb * 8 + swz8(rb, c)], sa[ra * 8 + swz8(ra, c)], acc);
-    }
-    __syncthreads();
-  }
-  const int id = s_row[wm * 32 + (lane & 31)];
-  if (id < 0) return;
+// One 32 x 32 block of outputs: lane l holds, of row l & 31, columns n + 8 g + 4 (l >> 5) + i in register 4 g + i.
+// id, id_lo, id_hi: the output rows of block rows l & 31, l & 15 and 16 + (l & 15) (< 0: not stored); sa: the row's
+// scale, sb: the block's 32 column scales in LDS.  All lanes take part.
+template <bool I8, bool F32, bool EPI, class A>
+__device__ __forceinline__ void store_block(const ProductArgs& p, int id, int id_lo, int id_hi, float sa,
+                                            const float* sb, int n, int lane, const A& acc) {
+  const int h = lane >> 5;
+  float v[4][4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const int n = n0 + wn * 32 + 8 * g + 4 * (lane >> 5);
-    if (n < p.N) store4<I8>(p, id, expert, n, acc, 4 * g);
+    const int col = n + 8 * g + 4 * h;
+    if constexpr (I8) {
+      const float4 f4 = *reinterpret_cast<const float4*>(sb + 8 * g + 4 * h);
+      const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[g][i] = (float)acc[4 * g + i] * sa * f[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[g][i] = acc[4 * g + i];
+    }
+    if constexpr (EPI) {
+      const bool in = id >= 0 && col < p.N;
+      if (p.bias && in) {
+        const float4 b = *reinterpret_cast<const float4*>(p.bias + col);
+        v[g][0] += b.x, v[g][1] += b.y, v[g][2] += b.z, v[g][3] += b.w;
+      }
+      if (p.add && in) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p.add + (size_t)id * p.N + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[g][i] += bf16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+      }
+    }
+    if constexpr (F32) {
+      if (id >= 0 && col < p.N)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.c) + (size_t)id * p.N + col) =
+            make_float4(v[g][0], v[g][1], v[g][2], v[g][3]);
+    }
   }
+  if constexpr (!F32) {
+    // bf16: the lane halves exchange groups (a lane then holds 8 consecutive columns of its row, twice), then lanes
+    // 16 apart exchange these chunks, so that each of two stores writes 64 contiguous bytes of 16 rows
+    uint32_t w[2][4];
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      const auto x = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(v[g][0], v[g][1]), cvt_bf16x2(v[g + 1][0], v[g + 1][1]),
+                                                      false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(v[g][2], v[g][3]), cvt_bf16x2(v[g + 1][2], v[g + 1][3]),
+                                                      false, false);
+      w[g / 2][0] = x[0], w[g / 2][1] = y[0], w[g / 2][2] = x[1], w[g / 2][3] = y[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const auto x = __builtin_amdgcn_permlane16_swap(w[0][i], w[1][i], false, false);
+      w[0][i] = x[0], w[1][i] = x[1];
+    }
+    // lanes 0-15 and 32-47 now hold columns 8 h .. of their row pair, lanes 16-31 and 48-63 columns 16 + 8 h ..
+    const int col = n + 8 * h + (lane & 16);
+    uint16_t* c = static_cast<uint16_t*>(p.c);
+    if (id_lo >= 0 && col < p.N) *reinterpret_cast<u32x4*>(c + (size_t)id_lo * p.N + col) = u32x4{w[0][0], w[0][1], w[0][2], w[0][3]};
+    if (id_hi >= 0 && col < p.N) *reinterpret_cast<u32x4*>(c + (size_t)id_hi * p.N + col) = u32x4{w[1][0], w[1][1], w[1][2], w[1][3]};
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// Few rows (dense 8-bit products): a workgroup owns 16 columns and reads their weights once, straight into
+// registers.  Its four waves take every fourth 128-byte line of the rows (two 16 x 16 matrix instructions deep), U
+// lines at a time, and add their partial sums through LDS.
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+template <bool F32, bool EPI, int MT, int U>
+__global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
+  constexpr int W = 4;
+  __shared__ i32x4 part[W][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16, k0 = (lane >> 4) * 16;
+  const char* zeros = reinterpret_cast<const char*>(kZeros);
+  const char* b = static_cast<const char*>(p.b) + (size_t)min(n0 + (lane & 15), p.N - 1) * p.Kb;
+  const char* a[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    a[m] = static_cast<const char*>(p.a) + (size_t)min(16 * m + (lane & 15), p.P - 1) * p.Kb;
+  const int lines = (p.Kb + 127) / 128;
+  i32x4 acc[MT] = {};
+  for (int l0 = wave; l0 < lines; l0 += W * U) {
+    u32x4 fb[U][2], fa[MT][U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = (l0 + u * W) * 128 + h * 64 + k0;
+        const bool in = k < p.Kb;
+        fb[u][h] = *reinterpret_cast<const u32x4*>(in ? b + k : zeros);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) fa[m][u][h] = *reinterpret_cast<const u32x4*>(in ? a[m] + k : zeros);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fb[u][h]),
+                                                         __builtin_bit_cast(i32x4, fa[m][u][h]), acc[m], 0, 0, 0);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
+  __syncthreads();
+  // wave m adds and stores row block m: lane l holds, of row l & 15, columns 4 (l >> 4) + i
+  for (int m = wave; m < MT; m += W) {
+    const i32x4 s = (part[0][m][lane] + part[1][m][lane]) + (part[2][m][lane] + part[3][m][lane]);
+    const int id = 16 * m + (lane & 15), n = n0 + 4 * (lane >> 4);
+    if (id >= p.P || n >= p.N) continue;
+    const size_t at = (size_t)id * p.N + n;
+    const float sa = p.a_scale[id];
+    const float4 f = *reinterpret_cast<const float4*>(p.b_scale + n);
+    float v[4] = {(float)s[0] * sa * f.x, (float)s[1] * sa * f.y, (float)s[2] * sa * f.z, (float)s[3] * sa * f.w};
+    if constexpr (EPI) {
+      if (p.bias) {
+        const float4 t = *reinterpret_cast<const float4*>(p.bias + n);
+        v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
+      }
+      if (p.add) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p.add + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += bf16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+      }
+    }
+    if constexpr (F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.c) + at) =
+          u32x2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+  }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// Persistent kernel: BM x BN tiles, operands loaded straight into an S-stage ring in LDS, K steps of KCH 16-byte
+// chunks per row, loads S - 1 steps ahead also across items.
+
+// 16 (4) bytes per lane from src to LDS at lds_base + 16 (4) * lane; lds_base is wave-uniform.  Inline assembly, so
+// that the compiler's wait counts do not order LDS reads behind loads in flight; the K loop waits itself.
+__device__ __forceinline__ void to_lds16(const void* src, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(src) : "memory");
+}
+__device__ __forceinline__ void to_lds4(const void* src, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// 16-byte chunk swizzle of an LDS row of KCH chunks, the XOR term for a row (rows repeat every 16).
+template <int KCH>
+__device__ __forceinline__ int swz_term(int row) {
+  return KCH == 8 ? (((row >> 1) ^ ((row & 1) << 2)) & 7) : (((row >> 1) ^ (row >> 2)) & 3);
+}
+
+// Row tiles of an expert whose items run together over all column blocks, so that the 32 workgroups of an XCD read
+// few distinct rows and columns at a time.
+constexpr int kGroupM = 4;
+
+struct ProductItem {
+  int expert, first, rows, n0;
+};
+
+// The item list of a launch: experts in order, within an expert groups of kGroupM row tiles, within a group column
+// blocks, within a block the group's tiles.  Lane l of every wave keeps experts 4 l .. 4 l + 3 in registers.
+template <int BM, int BN>
+struct ProductList {
+  int nbn, total;
+  int first[4], count[4], start[4];  // start: index of the expert's first item
+
+  __device__ __forceinline__ void init(const ProductArgs& p, int lane) {
+    nbn = (p.N + BN - 1) / BN;
+    if (!p.off) {
+      total = ((p.P + BM - 1) / BM) * nbn;
+      return;
+    }
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      first[i] = count[i] = 0;
+      if (e < p.E) expert_range(p, e, first[i], count[i]);
+      start[i] = sum;
+      sum += ((count[i] + BM - 1) / BM) * nbn;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) start[i] += incl - sum;
+    total = __builtin_amdgcn_readlane(incl, 63);
+  }
+
+  __device__ __forceinline__ ProductItem at(const ProductArgs& p, int item) const {
+    ProductItem it;
+    int j = item, rows = p.P, base = 0;
+    it.expert = 0;
+    if (p.off) {
+      // experts that start at or before the item; the last of them holds it (empty ones start where the next does)
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(start[i] <= item));
+      // several experts may start here: the empty ones among them precede the one that holds the item
+      it.expert = min(n, p.E) - 1;
+      const int l = it.expert >> 2, q = it.expert & 3;
+      const int f = q == 0 ? first[0] : q == 1 ? first[1] : q == 2 ? first[2] : first[3];
+      const int c = q == 0 ? count[0] : q == 1 ? count[1] : q == 2 ? count[2] : count[3];
+      const int s = q == 0 ? start[0] : q == 1 ? start[1] : q == 2 ? start[2] : start[3];
+      base = __builtin_amdgcn_readlane(f, l);
+      rows = __builtin_amdgcn_readlane(c, l);
+      j -= __builtin_amdgcn_readlane(s, l);
+    }
+    const int tiles = (rows + BM - 1) / BM;
+    const int g = j / (kGroupM * nbn);
+    const int size = min(kGroupM, tiles - g * kGroupM);
+    const int rem = j - g * kGroupM * nbn;
+    const int m = g * kGroupM + rem % size;
+    it.n0 = (rem / size) * BN;
+    it.first = base + m * BM;
+    it.rows = min(BM, rows - m * BM);
+    return it;
+  }
+};
+
+template <bool I8, int BM, int BN, int WM, int WN, int KCH, int S>
+struct RingCfg {
+  static constexpr int NW = WM * WN, NT = NW * 64, MI = BM / WM / 32, NJ = BN / WN / 32;
+  static constexpr int RPI = 64 / KCH;  // rows one load instruction fills
+  static constexpr int NA = BM / RPI / NW, NB = BN / RPI / NW;  // load instructions per wave and step
+  static constexpr int STAGE = (BM + BN) * KCH;  // chunks
+  static constexpr int SUB = KCH / 2;  // matrix instructions deep per step
+  // LDS: stages, output rows of three items, scales of two items
+  static constexpr size_t LDS = (size_t)S * STAGE * 16 + 3 * BM * 4 + (I8 ? 2 * (BM + BN) * 4 : 0);
+  static constexpr int PER_CU = LDS * 2 <= 160 * 1024 ? 2 : 1;
+  static_assert(BM % (RPI * NW) == 0 && BN % (RPI * NW) == 0 && BN <= NT && BM <= NT && LDS <= 160 * 1024, "");
+};
+
+template <bool I8, bool F32, bool EPI, int BM, int BN, int WM, int WN, int KCH, int S>
+__global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
+  using C = RingCfg<I8, BM, BN, WM, WN, KCH, S>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  ProductList<BM, BN> list;
+  list.init(p, lane);
+  // each XCD takes one contiguous run of items, its workgroups every nslot-th of them
+  const int per = (list.total + kNumXcd - 1) / kNumXcd;
+  const int nslot = (int)gridDim.x / kNumXcd;
+  const int xcd = (int)blockIdx.x % kNumXcd;
+  const int begin = xcd * per + (int)blockIdx.x / kNumXcd;
+  const int end = min(list.total, (xcd + 1) * per);
+  if (begin >= end) return;
+  const int n_items = (end - begin + nslot - 1) / nslot;
+
+  u32x4* sm = reinterpret_cast<u32x4*>(smem);
+  int* s_ids = reinterpret_cast<int*>(smem + (size_t)S * C::STAGE * 16);  // [3][BM]
+  float* s_sa = reinterpret_cast<float*>(s_ids + 3 * BM);                // [2][BM]
+  float* s_sb = s_sa + 2 * BM;                                           // [2][BN]
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
+  const uint32_t lds_ids = lds0 + S * C::STAGE * 16, lds_sa = lds_ids + 3 * BM * 4, lds_sb = lds_sa + 2 * BM * 4;
+
+  // at least S - 1 steps per item (those behind the row's end read zeros), so that an item's row ids have landed
+  // when its loads begin and no buffer of an item is refilled before its epilogue
+  const int nk = max((p.Kb + KCH * 16 - 1) / (KCH * 16), S - 1);
+  const int full = p.Kb / (KCH * 16);  // steps without a tail
+
+  // ---- loads
+  ProductItem lit = {};  // the item being loaded
+  ProductItem nit = list.at(p, begin);  // the one after it
+  int l_index = -1, l_kb = nk;
+  const char* asrc[C::NA];
+  const char* bsrc[C::NB];
+  const int lrow = lane / KCH;  // row of this lane within a load instruction
+  auto chunk = [&](int r) { return (lane % KCH) ^ swz_term<KCH>(r); };  // logical chunk this lane fetches of row r
+
+  auto source = [&](const char* row, int r) {
+    const int off = l_kb * (KCH * 16);
+    return l_kb < full || off + chunk(r + lrow) * 16 < p.Kb ? row + off : reinterpret_cast<const char*>(kZeros);
+  };
+  auto load_ids = [&](int index, const ProductItem& it) {
+    const int r = wave * 64 + lane;
+    if (p.rows && r < BM)
+      to_lds4(p.rows + it.first + min(r, it.rows - 1), lds_ids + (uint32_t)((index % 3) * BM + wave * 64) * 4);
+  };
+  auto row_id = [&](int index, const ProductItem& it, int r) {  // output row of tile row r, -1: none
+    const int id = p.rows ? s_ids[(index % 3) * BM + r] : it.first + r;
+    return r < it.rows && (unsigned)id < (unsigned)p.R ? id : -1;
+  };
+  // starts the next item: sources of its rows; its scales and the row ids of the one after it into LDS
+  auto next_item = [&]() {
+    ++l_index;
+    l_kb = 0;
+    lit = nit;
+    if (l_index + 1 < n_items) {
+      nit = list.at(p, begin + (l_index + 1) * nslot);
+      load_ids(l_index + 1, nit);
+    }
+#pragma unroll
+    for (int q = 0; q < C::NA; ++q) {
+      const int r = (wave * C::NA + q) * C::RPI + lrow;
+      const int id = max(row_id(l_index, lit, r), 0);  // rows without data read row 0
+      asrc[q] = static_cast<const char*>(p.a) + (size_t)a_row(p, id) * p.Kb + chunk(r) * 16;
+    }
+#pragma unroll
+    for (int q = 0; q < C::NB; ++q) {
+      const int r = (wave * C::NB + q) * C::RPI + lrow;
+      const int n = min(lit.n0 + r, p.N - 1);
+      bsrc[q] = static_cast<const char*>(p.b) + ((size_t)lit.expert * p.N + n) * p.Kb + chunk(r) * 16;
+    }
+    if constexpr (I8) {
+      const int par = l_index & 1, r = wave * 64 + lane;
+      if (r < BM) to_lds4(p.a_scale + a_row(p, max(row_id(l_index, lit, r), 0)), lds_sa + (uint32_t)(par * BM + wave * 64) * 4);
+      if (r < BN)
+        to_lds4(p.b_scale + (size_t)lit.expert * p.N + min(lit.n0 + r, p.N - 1),
+                lds_sb + (uint32_t)(par * BN + wave * 64) * 4);
+    }
+  };
+  // the loads of one operand of a step; past the last item they read zeros
+  auto issue_a = [&](int slot) {
+    const uint32_t base = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * KCH) * 16;
+#pragma unroll
+    for (int q = 0; q < C::NA; ++q) to_lds16(source(asrc[q], (wave * C::NA + q) * C::RPI), base + (uint32_t)(q * C::RPI * KCH) * 16);
+  };
+  auto issue_b = [&](int slot) {
+    const uint32_t base = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * KCH) * 16;
+#pragma unroll
+    for (int q = 0; q < C::NB; ++q) to_lds16(source(bsrc[q], (wave * C::NB + q) * C::RPI), base + (uint32_t)(q * C::RPI * KCH) * 16);
+    ++l_kb;
+  };
+
+  // ---- fragments: tile row block b holds rows 32 b ..; blocks are dealt to the waves in turn, so that a partly
+  // filled tile gives every wave its share of the filled blocks
+  const int frow = lane & 31;
+  struct Frag {
+    u32x4 a[C::MI], b[C::NJ];
+  };
+  auto read_frags = [&](Frag& f, const u32x4* st, int sub) {
+    const int c = frow * KCH + ((2 * sub + (lane >> 5)) ^ swz_term<KCH>(frow));
+#pragma unroll
+    for (int m = 0; m < C::MI; ++m) f.a[m] = st[(m * WM + wm) * 32 * KCH + c];
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) f.b[j] = st[(BM + (wn * C::NJ + j) * 32) * KCH + c];
+  };
+
+  // ---- start: the first item's row ids, then S - 1 steps of loads
+  load_ids(0, nit);
+  wait_loads<0>();
+  __syncthreads();
+  next_item();
+  for (int i = 0; i < S - 1; ++i) {
+    issue_a(i);
+    issue_b(i);
+  }
+  int slot = 0;
+  for (int index = 0; index < n_items; ++index) {
+    // no load beyond this item has been issued yet (nk >= S - 1)
+    const ProductItem it = lit;
+    const int live = max(0, min(C::MI, ((it.rows + 31) / 32 - wm + WM - 1) / WM));
+    typename Acc<I8>::t32 acc[C::MI][C::NJ] = {};
+    auto mma = [&](const Frag& f) {
+#pragma unroll
+      for (int m = 0; m < C::MI; ++m)
+        if (m == 0 || m < live)
+#pragma unroll
+          for (int j = 0; j < C::NJ; ++j) acc[m][j] = mma32(f.b[j], f.a[m], acc[m][j]);
+    };
+    // one step's wait: the younger S - 2 steps may be in flight; then the loads of the step S - 1 ahead start
+    auto begin_step = [&]() {
+      wait_loads<(S - 2) * (C::NA + C::NB)>();
+      __syncthreads();
+      if (l_kb == nk && l_index + 1 < n_items) next_item();
+    };
+    if (live > 0) {
+      // straight-line body: a branch around LDS reads would make the compiler wait for all of them at each use
+      for (int kb = 0; kb < nk; ++kb) {
+        begin_step();
+        const u32x4* st = sm + slot * C::STAGE;
+        const int to = slot == 0 ? S - 1 : slot - 1;
+        Frag f[2];
+        read_frags(f[0], st, 0);
+        issue_a(to);
+        read_frags(f[1], st, 1);
+        mma(f[0]);
+        issue_b(to);
+#pragma unroll
+        for (int s = 1; s < C::SUB; ++s) {
+          if (s + 1 < C::SUB) read_frags(f[(s + 1) & 1], st, s + 1);
+          mma(f[s & 1]);
+        }
+        slot = slot == S - 1 ? 0 : slot + 1;
+      }
+    } else {
+      for (int kb = 0; kb < nk; ++kb) {
+        begin_step();
+        const int to = slot == 0 ? S - 1 : slot - 1;
+        issue_a(to);
+        issue_b(to);
+        slot = slot == S - 1 ? 0 : slot + 1;
+      }
+    }
+    // ---- epilogue
+#pragma unroll
+    for (int m = 0; m < C::MI; ++m) {
+      const int r = (m * WM + wm) * 32;
+      if (m >= live) break;
+      const int id = row_id(index, it, r + frow);
+      const int id_lo = row_id(index, it, r + (lane & 15)), id_hi = row_id(index, it, r + 16 + (lane & 15));
+      float sa = 1.0f;
+      if constexpr (I8) sa = s_sa[(index & 1) * BM + r + frow];
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) {
+        const int nl = (wn * C::NJ + j) * 32;
+        if (it.n0 + nl < p.N)
+          store_block<I8, F32, EPI>(p, id, id_lo, id_hi, sa, s_sb + (index & 1) * BN + nl, it.n0 + nl, lane, acc[m][j]);
+      }
+    }
+  }
+  wait_loads<0>();  // no load may reach LDS after the workgroup has ended
+}
+
+template <bool I8, bool F32, bool EPI, int BM, int BN, int WM, int WN, int S>
+hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
+  using C = RingCfg<I8, BM, BN, WM, WN, 8, S>;
+  const auto kernel = ring_kernel<I8, F32, EPI, BM, BN, WM, WN, 8, S>;
+  // more than 64 KB of LDS has to be allowed once per device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)C::LDS);
+    if (e != hipSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  kernel<<<256 * C::PER_CU, C::NT, C::LDS, st>>>(p);
+  return hipGetLastError();
+}
+
+// The tile of a launch: the one whose rounds over the 256 CUs take the least time.  A round's cost is the time of a
+// 128-byte K step in us, measured with all CUs busy (dense 8-bit, 8192 x 4096 x 4096: 128, 153, 195 and 328 us);
+// the 80 KB tiles run two to a CU, their cost is half a pair's.  Grouped launches count half a tile of padding per
+// expert.  Per tile 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128:
+//   dense 8-bit, K 2048: 300 x 1024 27 / 18 / 9.5 / 7.9 us, 512 x 4096 28 / 18 / 10.9 / 14.9, 2048 x 2048
+//   29 / 19.6 / 17.4 / 26, 4096 x 4096 42 / 46 / 56 / 90
+//   bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 101 / 79 / 74 / 68 us, 512 tokens 168 / 146 / 146 / 145,
+//   2048 tokens 222 / 199 / 216 / 268, 8192 tokens 390 / 397 / 497 / 763
+template <bool I8, bool F32, bool EPI>
+hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
+  static const struct {
+    int bm, bn;
+    float cost;
+  } tiles[] = {{256, 256, 2.0f}, {128, 256, 1.2f}, {64, 128, 0.4f}, {32, 128, 0.31f}};
+  int best = 0;
+  float least = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1 : (p.P + tiles[i].bm - 1) / tiles[i].bm;
+    const int64_t items = rows * ((p.N + tiles[i].bn - 1) / tiles[i].bn);
+    const float t = (float)((items + 255) / 256) * tiles[i].cost;
+    if (i == 0 || t < least) best = i, least = t;
+  }
+  switch (best) {
+    case 0: return ring_launch<I8, F32, EPI, 256, 256, 4, 2, 2>(p, st);
+    case 1: return ring_launch<I8, F32, EPI, 128, 256, 2, 4, 3>(p, st);
+    case 2: return ring_launch<I8, F32, EPI, 64, 128, 2, 2, 3>(p, st);
+    default: return ring_launch<I8, F32, EPI, 32, 128, 1, 4, 4>(p, st);
+  }
+}
+
+template <bool F32, bool EPI>
+hipError_t dense_i8_launch(const ProductArgs& p, hipStream_t st) {
+  // up to 64 rows: us of the few-rows kernel (one / four row blocks) against the best tile, K 2048: 1 x 4096 3.5 /
+  // 4.6 against 7.2, 33 x 1024 - / 5.8 against 7.5, 64 x 4096 - / 7.3 against 7.7
+  const unsigned blocks = (unsigned)((p.N + 15) / 16);
+  if (p.P <= 16) {
+    skinny_kernel<F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
+    return hipGetLastError();
+  }
+  if (p.P <= 64 && blocks <= 256) {
+    skinny_kernel<F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
+    return hipGetLastError();
+  }
+  return tiled_launch<true, F32, EPI>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_product(const ProductArgs& p, bool i8, hipStream_t st) {
-  const int64_t tiles = p.off ? p.P / 64 + (p.E < p.P ? p.E : p.P) : ((int64_t)p.P + 63) / 64;
-  const dim3 grid((unsigned)tiles, (unsigned)((p.N + 63) / 64));
-  if (i8)
-    product_kernel<true><<<grid, 256, 0, st>>>(p);
-  else
-    product_kernel<false><<<grid, 256, 0, st>>>(p);
-  return hipGetLastError();
+hipError_t launch_product(const ProductArgs& args, bool i8, hipStream_t st) {
+  ProductArgs p = args;
+  // m = floor(2^(31 + l) / d) + 1 with l = ceil(log2 d): floor(id m / 2^(31 + l)) = floor(id / d) for id < 2^31
+  if (p.a_div > 1) {
+    int l = 1;
+    while (l < 31 && (1u << l) < (unsigned)p.a_div) ++l;
+    p.div_mul = (unsigned)((1ull << (31 + l)) / (unsigned)p.a_div + 1);
+    p.div_shift = l - 1;
+  }
+  if (!i8) return p.c_f32 ? tiled_launch<false, true, false>(p, st) : tiled_launch<false, false, false>(p, st);
+  if (p.off) return p.c_f32 ? tiled_launch<true, true, false>(p, st) : tiled_launch<true, false, false>(p, st);
+  if (p.bias || p.add) return p.c_f32 ? dense_i8_launch<true, true>(p, st) : dense_i8_launch<false, true>(p, st);
+  return p.c_f32 ? dense_i8_launch<true, false>(p, st) : dense_i8_launch<false, false>(p, st);
 }
 
 }  // namespace moe
