@@ -126,6 +126,9 @@ def _stream(stream=None) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public property's time
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -300,29 +303,35 @@ def moe_combine(o, w, h_s, ws_down, s, T, H, k, I_s, y, stream=None):
 
 
 # ------------------------------------------------------------- operators around the layer
-def _need(name, t, dtypes, numel):
-    """Refuses a tensor the C ABI cannot tell from the right one: wrong type, too few elements, strided, or on
-    another device than the current one (whose stream the call is enqueued on).  None passes (the C ABI knows
-    which pointers it requires)."""
-    if t is None or isinstance(t, int):
-        return
+def _need(*tensors):
+    """Refuses tensors the C ABI cannot tell from the right ones: of another type, with too few elements, strided, or
+    on another device than the current one (whose stream the call is enqueued on).  Each is (name, tensor, dtype,
+    elements); None and raw pointers pass (the C ABI knows which pointers it requires)."""
     import torch
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(str(d) for d in dtypes)}")
-    if t.numel() < numel:
-        raise ValueError(f"{name} has {t.numel()} elements; {numel} needed")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+    dev = None
+    for name, t, dtype, numel in tensors:
+        if t is None or t.__class__ is int:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}; expected {dtype}")
+        if t.numel() < numel:
+            raise ValueError(f"{name} has {t.numel()} elements; {numel} needed")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        at = t.get_device()
+        if at >= 0 and dev is None:
+            dev = torch.cuda.current_device()
+        if at < 0 or at != dev:
+            raise ValueError(f"{name} is on {t.device}, not on the current GPU")
 
 
 def _type(name, t):
+    """(MOE_BF16 or MOE_F32, the torch type) of a residual stream or a product's output."""
     import torch
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
+    if t.dtype is torch.bfloat16:
+        return BF16, t.dtype
+    if t.dtype is torch.float32:
+        return F32, t.dtype
     raise ValueError(f"{name} is {t.dtype}; expected torch.bfloat16 or torch.float32")
 
 
@@ -330,75 +339,51 @@ def moe_block_norm(r, y, w_post, gate, w_pre, T, H, r_out, x, q, q_scale, r_scal
                    w_add: float = 0.0, eps: float = 1e-6, stream=None):
     """The type of r (bf16 or fp32) is that of r_out; gate has H elements (one row for all tokens) or T * H."""
     import torch
-    bf, n = (torch.bfloat16,), T * H
-    r_type = _type("r", r)
-    _need("r", r, (r.dtype,), n)
-    _need("y", y, bf, n)
-    _need("w_post", w_post, bf, H)
-    _need("w_pre", w_pre, bf, H)
-    _need("r_out", r_out, (r.dtype,), n)
-    _need("x", x, bf, n)
-    _need("q", q, (torch.int8,), n)
-    _need("q_scale", q_scale, (torch.float32,), T)
-    gate_rows = 1
-    if gate is not None:
-        gate_rows = 1 if gate.numel() == H else T
-        _need("gate", gate, bf, gate_rows * H)
+    bf, n = torch.bfloat16, T * H
+    r_type, rt = _type("r", r)
+    gate_rows = 1 if gate is None or gate.numel() == H else T
+    _need(("r", r, rt, n), ("y", y, bf, n), ("w_post", w_post, bf, H), ("gate", gate, bf, gate_rows * H),
+          ("w_pre", w_pre, bf, H), ("r_out", r_out, rt, n), ("x", x, bf, n), ("q", q, torch.int8, n),
+          ("q_scale", q_scale, torch.float32, T))
     _check(lib().moe_block_norm(_p(r), r_type, _p(y), _p(w_post), _p(gate), gate_rows, r_scale, y_scale, _p(w_pre),
                                 w_add, eps, T, H, _p(r_out), _p(x), _p(q), _p(q_scale), _stream(stream)))
 
 
 def moe_quantize_i8(x, R, K, q, scale, stream=None):
     import torch
-    _need("x", x, (torch.bfloat16,), R * K)
-    _need("q", q, (torch.int8,), R * K)
-    _need("scale", scale, (torch.float32,), R)
+    _need(("x", x, torch.bfloat16, R * K), ("q", q, torch.int8, R * K), ("scale", scale, torch.float32, R))
     _check(lib().moe_quantize_i8(_p(x), R, K, _p(q), _p(scale), _stream(stream)))
 
 
 def moe_swiglu_i8(gu, row_gate, R, I, q, scale, stream=None):
     import torch
-    _need("gu", gu, (torch.bfloat16,), 2 * R * I)
-    _need("row_gate", row_gate, (torch.float32,), R)
-    _need("q", q, (torch.int8,), R * I)
-    _need("scale", scale, (torch.float32,), R)
+    _need(("gu", gu, torch.bfloat16, 2 * R * I), ("row_gate", row_gate, torch.float32, R),
+          ("q", q, torch.int8, R * I), ("scale", scale, torch.float32, R))
     _check(lib().moe_swiglu_i8(_p(gu), _p(row_gate), R, I, _p(q), _p(scale), _stream(stream)))
 
 
 def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
     """The type of c (bf16 or fp32) is the output's."""
     import torch
-    i8, f32 = (torch.int8,), (torch.float32,)
-    c_type = _type("c", c)
-    _need("a", a, i8, M * K)
-    _need("a_scale", a_scale, f32, M)
-    _need("b", b, i8, N * K)
-    _need("b_scale", b_scale, f32, N)
-    _need("bias", bias, f32, N)
-    _need("add", add, (torch.bfloat16,), M * N)
-    _need("c", c, (c.dtype,), M * N)
+    i8, f32 = torch.int8, torch.float32
+    c_type, ct = _type("c", c)
+    _need(("a", a, i8, M * K), ("a_scale", a_scale, f32, M), ("b", b, i8, N * K), ("b_scale", b_scale, f32, N),
+          ("bias", bias, f32, N), ("add", add, torch.bfloat16, M * N), ("c", c, ct, M * N))
     _check(lib().moe_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(bias), _p(add), M, N, K, _p(c), c_type,
                              _stream(stream)))
 
 
-def _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, dtype):
-    import torch
-    i32 = (torch.int32,)
-    a_rows = (R - 1) // a_div + 1 if R > 0 and a_div > 0 else 0
-    _need("a", a, dtype, a_rows * K)
-    _need("b", b, dtype, E * N * K)
-    _need("off", off, i32, E + 1)
-    _need("counts", counts, i32, E)
-    _need("rows", rows, i32, P)
-    _need("c", c, (c.dtype,), R * N)
-    return a_rows
+def _a_rows(a_div, R):
+    return (R - 1) // a_div + 1 if R > 0 and a_div > 0 else 0
 
 
 def moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, stream=None):
     """The type of c (bf16 or fp32) is the output's."""
     import torch
-    c_type = _type("c", c)
-    _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, (torch.bfloat16,))
+    bf, i32 = torch.bfloat16, torch.int32
+    c_type, ct = _type("c", c)
+    _need(("a", a, bf, _a_rows(a_div, R) * K), ("b", b, bf, E * N * K), ("off", off, i32, E + 1),
+          ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
     _check(lib().moe_grouped_gemm(_p(a), _p(b), _p(off), _p(counts), _p(rows), a_div, P, R, E, N, K, _p(c), c_type,
                                   _stream(stream)))
 
@@ -406,9 +391,10 @@ def moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, stream=No
 def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, stream=None):
     """The type of c (bf16 or fp32) is the output's."""
     import torch
-    c_type = _type("c", c)
-    a_rows = _need_grouped(a, b, off, counts, rows, a_div, P, R, E, N, K, c, (torch.int8,))
-    _need("a_scale", a_scale, (torch.float32,), a_rows)
-    _need("b_scale", b_scale, (torch.float32,), E * N)
+    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    c_type, ct = _type("c", c)
+    n = _a_rows(a_div, R)
+    _need(("a", a, i8, n * K), ("a_scale", a_scale, f32, n), ("b", b, i8, E * N * K), ("b_scale", b_scale, f32, E * N),
+          ("off", off, i32, E + 1), ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
     _check(lib().moe_grouped_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(off), _p(counts), _p(rows), a_div, P,
                                      R, E, N, K, _p(c), c_type, _stream(stream)))
