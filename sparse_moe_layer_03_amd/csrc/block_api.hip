@@ -114,13 +114,13 @@ int moe_block_norm(const void* r, int r_type, const uint16_t* y, const uint16_t*
   if (r_type != MOE_BF16 && r_type != MOE_F32)
     return fail(MOE_ERR_SHAPE, "%s: r_type=%d is neither MOE_BF16 nor MOE_F32", f, r_type);
   if (!(eps >= 0.0f)) return fail(MOE_ERR_SHAPE, "%s: eps must not be negative", f);
+  if (T == 0) return ok();  // tensors without elements have no address
   if (!y && (w_post || gate)) return fail(MOE_ERR_SHAPE, "%s: w_post or gate given without y", f);
   if (gate && gate_rows != 1 && gate_rows != T)
     return fail(MOE_ERR_SHAPE, "%s: gate_rows=%d must be 1 or T=%d", f, gate_rows, T);
   if ((q == nullptr) != (q_scale == nullptr)) return fail(MOE_ERR_NULL, "%s: q and q_scale go together", f);
   if ((w_pre != nullptr) != (x || q)) return fail(MOE_ERR_NULL, "%s: w_pre goes together with x or q", f);
   if (!r_out && !w_pre) return fail(MOE_ERR_NULL, "%s: no output", f);
-  if (T == 0) return ok();
   if (!r) return fail(MOE_ERR_NULL, "%s: r is required", f);
   for (const void* p : {r, (const void*)y, (const void*)w_post, (const void*)gate, (const void*)w_pre,
                         (const void*)r_out, (const void*)x, (const void*)q, (const void*)q_scale})

@@ -46,14 +46,20 @@ class DeviceLayer:
     ``<key>_scale`` row scales of ``weights``); ``forward`` then calls
     ``moe_forward_fp8``.  ``q4``: likewise the 4-bit weights (``<key>_q4``
     codes and ``<key>_q4scale`` fp16 group scales) and ``moe_forward_q4``.
+    ``i8``: the expert weights are quantised on the GPU to 8-bit integers with
+    a scale per output row, and ``forward`` runs the experts in 8-bit integers
+    with a scale per token, by the grouped products (see ``_forward_i8``).
     """
 
     def __init__(self, weights: Dict[str, np.ndarray], k: int, device="cuda:0", fp8: bool = False,
-                 q4: bool = False):
+                 q4: bool = False, i8: bool = False):
         import torch
+        if fp8 + q4 + i8 > 1:
+            raise ValueError("choose one of fp8, q4 and i8")
         self.device = torch.device(device)
         self.fp8 = fp8
         self.q4 = q4
+        self.i8 = i8
         self.w = {key: to_device_bf16(weights.get(key), self.device) for key in BF16_KEYS}
         self.q = {}
         if fp8:
@@ -77,17 +83,45 @@ class DeviceLayer:
         self._ws = None
         self._ws_bytes = 0
         self._ws_streams = []  # streams the current workspace has been used on since it was allocated
+        self._i8_views = None  # (workspace address, T, the views forward uses) of 8-bit layers
+        if i8:
+            self._quantize_weights()
 
     @classmethod
-    def from_inputs(cls, inp, device="cuda:0", fp8: bool = False, q4: bool = False):
-        return cls(inp, inp["wl"].k, device, fp8=fp8, q4=q4)
+    def from_inputs(cls, inp, device="cuda:0", fp8: bool = False, q4: bool = False, i8: bool = False):
+        return cls(inp, inp["wl"].k, device, fp8=fp8, q4=q4, i8=i8)
+
+    def _quantize_weights(self):
+        """8-bit codes and row scales of the expert weights, gate and up rows of an expert one after the other."""
+        import torch
+        s, W = self.shapes, self.w
+
+        def rows(a, n, K):
+            q = torch.empty((n, K), dtype=torch.int8, device=self.device)
+            sc = torch.empty(n, dtype=torch.float32, device=self.device)
+            moe.moe_quantize_i8(a, n, K, q, sc)
+            return q, sc
+
+        def stacked(gate, up, E, I, K):
+            (g, gs), (u, us) = rows(gate, E * I, K), rows(up, E * I, K)
+            return (torch.cat([g.view(E, I, K), u.view(E, I, K)], dim=1).view(E * 2 * I, K),
+                    torch.cat([gs.view(E, I), us.view(E, I)], dim=1).reshape(-1))
+        with torch.cuda.device(self.device):
+            self.q["gu"], self.q["gu_scale"] = stacked(W["w_gate"], W["w_up"], s.E, s.I, s.H)
+            self.q["down"], self.q["down_scale"] = rows(W["w_down"], s.E * s.H, s.I)
+            if s.I_s:
+                self.q["s_gu"], self.q["s_gu_scale"] = stacked(W["ws_gate"], W["ws_up"], 1, s.I_s, s.H)
+                self.q["s_down"], self.q["s_down_scale"] = rows(W["ws_down"], s.H, s.I_s)
 
     def workspace(self, T: int):
-        import torch
         s = self.shapes
         need = moe.moe_workspace_size(T, s.H, s.E, s.k, s.I, s.I_s)
         if need == 0 and T > 0:
             raise moe.MoEError(moe.MOE_ERR_SHAPE, "unsupported shapes")
+        return self._reserve(need)
+
+    def _reserve(self, need: int):
+        import torch
         if self._ws is None or self._ws_bytes < need:
             if self._ws is not None:
                 # the caching allocator tracks only the allocating stream: keep the old buffer from being
@@ -118,6 +152,8 @@ class DeviceLayer:
         T = x.shape[0]
         if y is None:
             y = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
+        if self.i8:
+            return self._forward_i8(x, y, stream)
         ws, nbytes = self.workspace(T)
         self._note_stream(stream)
         W = self.w
@@ -144,8 +180,93 @@ class DeviceLayer:
         from the workspace."""
         import torch
         s = self.shapes
+        if self.i8:
+            return self._i8_buffers(T)["ids"]
         off = moe.moe_forward_ids_offset(T, s.H, s.E, s.k, s.I, s.I_s)
         return self._ws[off:off + T * s.k * 4].view(torch.int32).view(T, s.k)
+
+    # ---------------------------------------------------------------- 8-bit experts
+    def _i8_buffers(self, T: int):
+        """The 8-bit forward's intermediates for T tokens, views of the layer's workspace."""
+        import torch
+        s = self.shapes
+        n, E = T * s.k, s.E
+        i32, f32, i8, bf, u8 = torch.int32, torch.float32, torch.int8, torch.bfloat16, torch.uint8
+        rows = moe.moe_align_max_rows(T, E, s.k)
+        want = {"ids": (i32, T, s.k), "w": (f32, T, s.k), "s": (f32, T), "counts": (i32, E), "pad_off": (i32, E + 1),
+                "sorted": (i32, rows), "inv": (i32, n), "tiles": (i32, 2 * moe.moe_align_max_tiles(T, E, s.k)),
+                "n_tiles": (i32, 2), "scratch": (u8, moe.moe_align_scratch_size(T, E, s.k)),
+                "route_scratch": (u8, moe.moe_route_scratch_size(T, s.H, E)),
+                "xq": (i8, T, s.H), "xs": (f32, T), "gu": (bf, n, 2 * s.I), "hq": (i8, n, s.I), "hs": (f32, n),
+                "o": (bf, n, s.H)}
+        if s.I_s:
+            want.update({"s_gu": (bf, T, 2 * s.I_s), "s_hq": (i8, T, s.I_s), "s_hs": (f32, T)})
+        at, place = 0, {}
+        for name, (dtype, *shape) in want.items():
+            nbytes = int(np.prod(shape)) * dtype.itemsize
+            place[name] = (at, nbytes)
+            at += -(-nbytes // 256) * 256
+        ws, _ = self._reserve(at)
+        if self._i8_views is None or self._i8_views[:2] != (ws.data_ptr(), T):
+            views = {name: ws[place[name][0]:place[name][0] + place[name][1]].view(dtype).view(*shape)
+                     for name, (dtype, *shape) in want.items()}
+            self._i8_views = (ws.data_ptr(), T, views)
+        return self._i8_views[2]
+
+    def _forward_i8(self, x, y, stream=None, quantized=False):
+        """The layer with its experts in 8-bit integers: routing on the bf16 tokens, then per token one quantisation
+        (unless ``xq`` and ``xs`` hold it already), the gate and up rows as one grouped product over the tokens of
+        each expert, SwiGLU quantised per assignment, the grouped down product, and the combine.  The shared
+        expert's products are dense; its gate multiplies the scales of its SwiGLU rows, and its down product adds
+        the routed experts' output, which has been rounded to bf16 once by the combine."""
+        s, q = self.shapes, self.q
+        T = x.shape[0]
+        if T == 0:
+            return y
+        b = self._i8_buffers(T)
+        self._note_stream(stream)
+        n, E = T * s.k, s.E
+        moe.moe_route(x, self.w["w_router"], self.bias, self.w["w_sg"], T, s.H, E, s.k, b["ids"], b["w"],
+                      b["s"] if s.I_s else None, None, stream, scratch=b["route_scratch"])
+        moe.moe_align(b["ids"], T, E, s.k, b["counts"], b["pad_off"], b["sorted"], b["inv"], b["tiles"],
+                      b["n_tiles"], b["scratch"], b["scratch"].numel(), stream)
+        if not quantized:
+            moe.moe_quantize_i8(x, T, s.H, b["xq"], b["xs"], stream)
+        P = b["sorted"].numel()
+        moe.moe_grouped_gemm_i8(b["xq"], b["xs"], q["gu"], q["gu_scale"], b["pad_off"], b["counts"], b["sorted"], s.k,
+                                P, n, E, 2 * s.I, s.H, b["gu"], stream)
+        moe.moe_swiglu_i8(b["gu"], None, n, s.I, b["hq"], b["hs"], stream)
+        moe.moe_grouped_gemm_i8(b["hq"], b["hs"], q["down"], q["down_scale"], b["pad_off"], b["counts"], b["sorted"],
+                                1, P, n, E, s.H, s.I, b["o"], stream)
+        moe.moe_combine(b["o"], b["w"], None, None, None, T, s.H, s.k, 0, y, stream)
+        if s.I_s:
+            moe.moe_gemm_i8(b["xq"], b["xs"], q["s_gu"], q["s_gu_scale"], None, None, T, 2 * s.I_s, s.H, b["s_gu"],
+                            stream)
+            moe.moe_swiglu_i8(b["s_gu"], b["s"], T, s.I_s, b["s_hq"], b["s_hs"], stream)
+            moe.moe_gemm_i8(b["s_hq"], b["s_hs"], q["s_down"], q["s_down_scale"], None, y, T, s.H, s.I_s, y, stream)
+        return y
+
+    def forward_block(self, r, y, w_pre, w_post=None, gate=None, r_scale: float = 1.0, y_scale: float = 1.0,
+                      w_add: float = 0.0, eps: float = 1e-6, out=None, stream=None):
+        """The layer as a block of a residual stream: r (in place) takes the previous block's output y (None: it has
+        none) through moe_block_norm, and the layer runs on the normalised rows.  Returns the layer's output, which
+        the next block's moe_block_norm adds to r.  8-bit layers take the norm's quantised rows as they are."""
+        import torch
+        s = self.shapes
+        T = r.shape[0]
+        # x belongs to the pool of the stream that uses it
+        st = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(st):
+            x = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
+        b = self._i8_buffers(T) if self.i8 and T > 0 else {"xq": None, "xs": None}
+        moe.moe_block_norm(r, y, w_post, gate, w_pre, T, s.H, r, x, b["xq"], b["xs"], r_scale, y_scale, w_add, eps,
+                           stream)
+        if not self.i8:
+            out = self.forward(x, out, stream)
+        else:
+            out = torch.empty_like(x) if out is None else out
+            self._forward_i8(x, out, stream, quantized=True)
+        return out
 
     # ---------------------------------------------------------------- stages
     def alloc_stage_buffers(self, T: int):
@@ -245,6 +366,8 @@ class PrefillRunner:
         if layer.q4:
             raise ValueError("the prefill runner takes BF16 or FP8 weights (4-bit weights serve T <= %d)"
                              % moe.Q4_MAX_T)
+        if layer.i8:
+            raise ValueError("the prefill runner takes BF16 or FP8 weights")
         if layer.fp8:
             q = layer.q
             self.handle = moe.moe_prefill_runner_create_fp8(
