@@ -229,9 +229,17 @@ __device__ __forceinline__ void to_lds16(const void* src, uint32_t lds_base) {
 __device__ __forceinline__ void to_lds4(const void* src, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(src) : "memory");
 }
-// The same past the caches.
-__device__ __forceinline__ void to_lds16_nt(const void* src, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds_base), "v"(src) : "memory");
+// The K loop's form: a wave-uniform base and 32-bit lane offsets that stay the same from step to step, so that a load
+// costs no vector instruction (dense 8-bit 8192 x 4096 x 4096 128 -> 120 us, grouped bf16 prefill 394 -> 373 us).
+// NT: past the caches.
+template <bool NT>
+__device__ __forceinline__ void to_lds16(const char* base, uint32_t off, uint32_t lds_base) {
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds_base), "v"(off), "s"(base)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
+                 : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -331,7 +339,7 @@ struct RingCfg {
   static_assert(BM % (RPI * NW) == 0 && BN % (RPI * NW) == 0 && BN <= NT && BM <= NT && LDS <= 160 * 1024, "");
 };
 
-template <bool I8, bool F32, bool EPI, bool NT, int BM, int BN, int WM, int WN, int KCH, int S>
+template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int KCH, int S>
 __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   using C = RingCfg<I8, EPI, BM, BN, WM, WN, KCH, S>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -361,20 +369,22 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   // at least S - 1 steps per item (those behind the row's end read zeros), so that an item's row ids have landed
   // when its loads begin and no buffer of an item is refilled before its epilogue
   const int nk = max((p.Kb + KCH * 16 - 1) / (KCH * 16), S - 1);
-  const int full = p.Kb / (KCH * 16);  // steps without a tail
 
   // ---- loads
   ProductItem lit = {};  // the item being loaded
   ProductItem nit = list.at(p, begin);  // the one after it
   int l_index = -1, l_kb = nk;
-  const char* asrc[C::NA];
-  const char* bsrc[C::NB];
+  // byte offsets of this lane's rows from A and from the item's first B row
+  std::conditional_t<TAIL, uint64_t, uint32_t> aoff[C::NA];
+  uint32_t boff[C::NB];
+  const char* abase = static_cast<const char*>(p.a);
+  const char* bbase = abase;
   const int lrow = lane / KCH;  // row of this lane within a load instruction
   auto chunk = [&](int r) { return (lane % KCH) ^ swz_term<KCH>(r); };  // logical chunk this lane fetches of row r
-
-  auto source = [&](const char* row, int r) {
-    const int off = l_kb * (KCH * 16);
-    return l_kb < full || off + chunk(r + lrow) * 16 < p.Kb ? row + off : reinterpret_cast<const char*>(kZeros);
+  // this lane's 16 bytes at off, or zeros where they lie behind the row's end; r: the load's first tile row
+  auto source = [&](const char* base, uint64_t off, int r) {
+    const int k = l_kb * (KCH * 16);
+    return k + chunk(r + lrow) * 16 < p.Kb ? base + off + k : reinterpret_cast<const char*>(kZeros);
   };
   auto load_ids = [&](int index, const ProductItem& it) {
     const int r = wave * 64 + lane;
@@ -398,13 +408,13 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
     for (int q = 0; q < C::NA; ++q) {
       const int r = (wave * C::NA + q) * C::RPI + lrow;
       const int id = max(row_id(l_index, lit, r), 0);  // rows without data read row 0
-      asrc[q] = static_cast<const char*>(p.a) + (size_t)a_row(p, id) * p.Kb + chunk(r) * 16;
+      aoff[q] = (decltype(aoff[q] + 0))((uint64_t)a_row(p, id) * p.Kb + chunk(r) * 16);
     }
+    bbase = static_cast<const char*>(p.b) + ((size_t)lit.expert * p.N + lit.n0) * p.Kb;
 #pragma unroll
     for (int q = 0; q < C::NB; ++q) {
       const int r = (wave * C::NB + q) * C::RPI + lrow;
-      const int n = min(lit.n0 + r, p.N - 1);
-      bsrc[q] = static_cast<const char*>(p.b) + ((size_t)lit.expert * p.N + n) * p.Kb + chunk(r) * 16;
+      boff[q] = (uint32_t)(min(r, p.N - 1 - lit.n0) * p.Kb + chunk(r) * 16);
     }
     if constexpr (I8) {
       const int par = l_index & 1, r = wave * 64 + lane;
@@ -417,22 +427,34 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
                 lds_bias + (uint32_t)(par * BN + wave * 64) * 4);
     }
   };
-  // the loads of one operand of a step; past the last item they read zeros
+  // the loads of one operand of a step; behind the last item they repeat its last step (TAIL: read zeros)
   auto issue_a = [&](int slot) {
-    const uint32_t base = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * KCH) * 16;
+    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * KCH) * 16;
+    const char* base = abase + min(l_kb, nk - 1) * (KCH * 16);
 #pragma unroll
-    for (int q = 0; q < C::NA; ++q) to_lds16(source(asrc[q], (wave * C::NA + q) * C::RPI), base + (uint32_t)(q * C::RPI * KCH) * 16);
+    for (int q = 0; q < C::NA; ++q) {
+      const uint32_t at = dst + (uint32_t)(q * C::RPI * KCH) * 16;
+      if constexpr (TAIL)
+        to_lds16(source(abase, aoff[q], (wave * C::NA + q) * C::RPI), at);
+      else
+        to_lds16<false>(base, aoff[q], at);
+    }
   };
   auto issue_b = [&](int slot) {
-    const uint32_t base = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * KCH) * 16;
+    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * KCH) * 16;
+    const char* base = bbase + min(l_kb, nk - 1) * (KCH * 16);
+    if (NT && !TAIL && lit.only) {
 #pragma unroll
-    for (int q = 0; q < C::NB; ++q) {
-      const void* src = source(bsrc[q], (wave * C::NB + q) * C::RPI);
-      const uint32_t dst = base + (uint32_t)(q * C::RPI * KCH) * 16;
-      if (NT && lit.only)
-        to_lds16_nt(src, dst);
-      else
-        to_lds16(src, dst);
+      for (int q = 0; q < C::NB; ++q) to_lds16<true>(base, boff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::NB; ++q) {
+        const uint32_t at = dst + (uint32_t)(q * C::RPI * KCH) * 16;
+        if constexpr (TAIL)
+          to_lds16(source(bbase, boff[q], (wave * C::NB + q) * C::RPI), at);
+        else
+          to_lds16<false>(base, boff[q], at);
+      }
     }
     ++l_kb;
   };
@@ -532,10 +554,10 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   wait_loads<0>();  // no load may reach LDS after the workgroup has ended
 }
 
-template <bool I8, bool F32, bool EPI, bool NT, int BM, int BN, int WM, int WN, int S>
-hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
+template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
+hipError_t ring_run(const ProductArgs& p, hipStream_t st) {
   using C = RingCfg<I8, EPI, BM, BN, WM, WN, 8, S>;
-  const auto kernel = ring_kernel<I8, F32, EPI, NT, BM, BN, WM, WN, 8, S>;
+  const auto kernel = ring_kernel<I8, F32, EPI, NT, TAIL, BM, BN, WM, WN, 8, S>;
   // more than 64 KB of LDS has to be allowed once per device
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
@@ -552,6 +574,16 @@ hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Rows that are whole steps, of which there are enough to fill the ring, and A offsets of 32 bits take the form
+// without tail handling.
+template <bool I8, bool F32, bool EPI, bool NT, int BM, int BN, int WM, int WN, int S>
+hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
+  const int64_t a_rows = ((int64_t)p.R - 1) / p.a_div + 1;
+  if (p.Kb % 128 == 0 && p.Kb / 128 >= S - 1 && a_rows * p.Kb <= ((int64_t)1 << 32))
+    return ring_run<I8, F32, EPI, NT, false, BM, BN, WM, WN, S>(p, st);
+  return ring_run<I8, F32, EPI, false, true, BM, BN, WM, WN, S>(p, st);
+}
+
 // The tile of a launch: the one whose rounds over the 256 CUs take the least time.  A round's cost is the time of a
 // 128-byte K step in us, measured with all CUs busy (dense 8-bit, 8192 x 4096 x 4096: 128, 153, 195 and 328 us);
 // the 80 KB tiles run two to a CU, their cost is half a pair's.  Grouped launches count half a tile of padding per
@@ -565,7 +597,7 @@ hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
   static const struct {
     int bm, bn;
     float cost;
-  } tiles[] = {{256, 256, 1.95f}, {128, 256, 1.2f}, {64, 128, 0.42f}, {32, 128, 0.34f}};
+  } tiles[] = {{256, 256, 1.95f}, {128, 256, 1.2f}, {64, 128, 0.46f}, {32, 128, 0.37f}};
   int best = 0;
   float least = 0.0f;
   for (int i = 0; i < 4; ++i) {

@@ -125,11 +125,24 @@ def _p(t) -> Optional[int]:
 def _stream(stream=None) -> Optional[int]:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    return _raw_stream(_device())
+
+
+# The current device and its current stream: torch's own functions behind the public ones, which take a tenth of their
+# time.  Bound at the first call, when torch has initialised the GPU.
+def _device() -> int:
+    global _device, _raw_stream
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public property's time
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    at = torch.cuda.current_device()
+    get, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if get is not None and raw is not None:
+        _device, _raw_stream = get, raw
+    return at
+
+
+def _raw_stream(device: int) -> int:
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 # ------------------------------------------------------------- sizes
@@ -303,26 +316,33 @@ def moe_combine(o, w, h_s, ws_down, s, T, H, k, I_s, y, stream=None):
 
 
 # ------------------------------------------------------------- operators around the layer
-def _need(*tensors):
-    """Refuses tensors the C ABI cannot tell from the right ones: of another type, with too few elements, strided, or
-    on another device than the current one (whose stream the call is enqueued on).  Each is (name, tensor, dtype,
-    elements); None and raw pointers pass (the C ABI knows which pointers it requires)."""
-    import torch
-    dev = None
+def _args(*tensors):
+    """Device pointers of tensors, given as (name, tensor, dtype, elements) (None stays NULL, raw pointers pass).
+    Refuses what the C ABI cannot tell from the right tensor: another type, too few elements, strides, or another
+    device than the current one (whose stream the call is enqueued on)."""
+    out = []
+    at = set()
     for name, t, dtype, numel in tensors:
         if t is None or t.__class__ is int:
-            continue
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} is {t.dtype}; expected {dtype}")
-        if t.numel() < numel:
-            raise ValueError(f"{name} has {t.numel()} elements; {numel} needed")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        at = t.get_device()
-        if at >= 0 and dev is None:
-            dev = torch.cuda.current_device()
-        if at < 0 or at != dev:
-            raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+            out.append(t)
+        elif t.dtype is dtype and t.numel() >= numel and t.is_contiguous() and t.is_cuda:
+            out.append(t.data_ptr())
+            at.add(t.get_device())
+        else:
+            raise ValueError(_fault(name, t, dtype, numel))
+    if at and at != {_device()}:
+        raise ValueError(f"tensors on GPU {sorted(at)}; the current one is {_device()}")
+    return out
+
+
+def _fault(name, t, dtype, numel) -> str:
+    if t.dtype is not dtype:
+        return f"{name} is {t.dtype}; expected {dtype}"
+    if t.numel() < numel:
+        return f"{name} has {t.numel()} elements; {numel} needed"
+    if not t.is_contiguous():
+        return f"{name} must be contiguous"
+    return f"{name} is on {t.device}, not on a GPU"
 
 
 def _type(name, t):
@@ -342,24 +362,26 @@ def moe_block_norm(r, y, w_post, gate, w_pre, T, H, r_out, x, q, q_scale, r_scal
     bf, n = torch.bfloat16, T * H
     r_type, rt = _type("r", r)
     gate_rows = 1 if gate is None or gate.numel() == H else T
-    _need(("r", r, rt, n), ("y", y, bf, n), ("w_post", w_post, bf, H), ("gate", gate, bf, gate_rows * H),
-          ("w_pre", w_pre, bf, H), ("r_out", r_out, rt, n), ("x", x, bf, n), ("q", q, torch.int8, n),
-          ("q_scale", q_scale, torch.float32, T))
-    _check(lib().moe_block_norm(_p(r), r_type, _p(y), _p(w_post), _p(gate), gate_rows, r_scale, y_scale, _p(w_pre),
-                                w_add, eps, T, H, _p(r_out), _p(x), _p(q), _p(q_scale), _stream(stream)))
+    r, y, w_post, gate, w_pre, r_out, x, q, q_scale = _args(
+        ("r", r, rt, n), ("y", y, bf, n), ("w_post", w_post, bf, H), ("gate", gate, bf, gate_rows * H),
+        ("w_pre", w_pre, bf, H), ("r_out", r_out, rt, n), ("x", x, bf, n), ("q", q, torch.int8, n),
+        ("q_scale", q_scale, torch.float32, T))
+    _check(lib().moe_block_norm(r, r_type, y, w_post, gate, gate_rows, r_scale, y_scale, w_pre, w_add, eps, T, H, r_out,
+                                x, q, q_scale, _stream(stream)))
 
 
 def moe_quantize_i8(x, R, K, q, scale, stream=None):
     import torch
-    _need(("x", x, torch.bfloat16, R * K), ("q", q, torch.int8, R * K), ("scale", scale, torch.float32, R))
-    _check(lib().moe_quantize_i8(_p(x), R, K, _p(q), _p(scale), _stream(stream)))
+    x, q, scale = _args(("x", x, torch.bfloat16, R * K), ("q", q, torch.int8, R * K),
+                        ("scale", scale, torch.float32, R))
+    _check(lib().moe_quantize_i8(x, R, K, q, scale, _stream(stream)))
 
 
 def moe_swiglu_i8(gu, row_gate, R, I, q, scale, stream=None):
     import torch
-    _need(("gu", gu, torch.bfloat16, 2 * R * I), ("row_gate", row_gate, torch.float32, R),
-          ("q", q, torch.int8, R * I), ("scale", scale, torch.float32, R))
-    _check(lib().moe_swiglu_i8(_p(gu), _p(row_gate), R, I, _p(q), _p(scale), _stream(stream)))
+    gu, row_gate, q, scale = _args(("gu", gu, torch.bfloat16, 2 * R * I), ("row_gate", row_gate, torch.float32, R),
+                                   ("q", q, torch.int8, R * I), ("scale", scale, torch.float32, R))
+    _check(lib().moe_swiglu_i8(gu, row_gate, R, I, q, scale, _stream(stream)))
 
 
 def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
@@ -367,10 +389,10 @@ def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
     import torch
     i8, f32 = torch.int8, torch.float32
     c_type, ct = _type("c", c)
-    _need(("a", a, i8, M * K), ("a_scale", a_scale, f32, M), ("b", b, i8, N * K), ("b_scale", b_scale, f32, N),
-          ("bias", bias, f32, N), ("add", add, torch.bfloat16, M * N), ("c", c, ct, M * N))
-    _check(lib().moe_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(bias), _p(add), M, N, K, _p(c), c_type,
-                             _stream(stream)))
+    a, a_scale, b, b_scale, bias, add, c = _args(
+        ("a", a, i8, M * K), ("a_scale", a_scale, f32, M), ("b", b, i8, N * K), ("b_scale", b_scale, f32, N),
+        ("bias", bias, f32, N), ("add", add, torch.bfloat16, M * N), ("c", c, ct, M * N))
+    _check(lib().moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, c_type, _stream(stream)))
 
 
 def _a_rows(a_div, R):
@@ -382,10 +404,10 @@ def moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, stream=No
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     c_type, ct = _type("c", c)
-    _need(("a", a, bf, _a_rows(a_div, R) * K), ("b", b, bf, E * N * K), ("off", off, i32, E + 1),
-          ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
-    _check(lib().moe_grouped_gemm(_p(a), _p(b), _p(off), _p(counts), _p(rows), a_div, P, R, E, N, K, _p(c), c_type,
-                                  _stream(stream)))
+    a, b, off, counts, rows, c = _args(
+        ("a", a, bf, _a_rows(a_div, R) * K), ("b", b, bf, E * N * K), ("off", off, i32, E + 1),
+        ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
+    _check(lib().moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, c_type, _stream(stream)))
 
 
 def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, stream=None):
@@ -394,7 +416,8 @@ def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, 
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
     c_type, ct = _type("c", c)
     n = _a_rows(a_div, R)
-    _need(("a", a, i8, n * K), ("a_scale", a_scale, f32, n), ("b", b, i8, E * N * K), ("b_scale", b_scale, f32, E * N),
-          ("off", off, i32, E + 1), ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
-    _check(lib().moe_grouped_gemm_i8(_p(a), _p(a_scale), _p(b), _p(b_scale), _p(off), _p(counts), _p(rows), a_div, P,
-                                     R, E, N, K, _p(c), c_type, _stream(stream)))
+    a, a_scale, b, b_scale, off, counts, rows, c = _args(
+        ("a", a, i8, n * K), ("a_scale", a_scale, f32, n), ("b", b, i8, E * N * K), ("b_scale", b_scale, f32, E * N),
+        ("off", off, i32, E + 1), ("counts", counts, i32, E), ("rows", rows, i32, P), ("c", c, ct, R * N))
+    _check(lib().moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, c_type,
+                                     _stream(stream)))
