@@ -369,6 +369,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   // at least S - 1 steps per item (those behind the row's end read zeros), so that an item's row ids have landed
   // when its loads begin and no buffer of an item is refilled before its epilogue
   const int nk = max((p.Kb + KCH * 16 - 1) / (KCH * 16), S - 1);
+  // TAIL: steps without a row's end in them, and whether every A offset fits 32 bits
+  const int full = p.Kb / (KCH * 16);
+  const bool narrow = !TAIL || ((uint64_t)a_row(p, p.R - 1) + 1) * p.Kb <= (1ull << 32);
 
   // ---- loads
   ProductItem lit = {};  // the item being loaded
@@ -427,34 +430,33 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
                 lds_bias + (uint32_t)(par * BN + wave * 64) * 4);
     }
   };
-  // the loads of one operand of a step; behind the last item they repeat its last step (TAIL: read zeros)
+  // The loads of one operand of a step.  Behind the last item they repeat its last step (TAIL: read zeros).
   auto issue_a = [&](int slot) {
     const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * KCH) * 16;
     const char* base = abase + min(l_kb, nk - 1) * (KCH * 16);
+    if (TAIL && (l_kb >= full || !narrow)) {
 #pragma unroll
-    for (int q = 0; q < C::NA; ++q) {
-      const uint32_t at = dst + (uint32_t)(q * C::RPI * KCH) * 16;
-      if constexpr (TAIL)
-        to_lds16(source(abase, aoff[q], (wave * C::NA + q) * C::RPI), at);
-      else
-        to_lds16<false>(base, aoff[q], at);
+      for (int q = 0; q < C::NA; ++q)
+        to_lds16(source(abase, aoff[q], (wave * C::NA + q) * C::RPI), dst + (uint32_t)(q * C::RPI * KCH) * 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < C::NA; ++q)
+        to_lds16<false>(base, (uint32_t)aoff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
     }
   };
   auto issue_b = [&](int slot) {
     const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * KCH) * 16;
     const char* base = bbase + min(l_kb, nk - 1) * (KCH * 16);
-    if (NT && !TAIL && lit.only) {
+    if (TAIL && l_kb >= full) {
+#pragma unroll
+      for (int q = 0; q < C::NB; ++q)
+        to_lds16(source(bbase, boff[q], (wave * C::NB + q) * C::RPI), dst + (uint32_t)(q * C::RPI * KCH) * 16);
+    } else if (NT && lit.only) {
 #pragma unroll
       for (int q = 0; q < C::NB; ++q) to_lds16<true>(base, boff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
     } else {
 #pragma unroll
-      for (int q = 0; q < C::NB; ++q) {
-        const uint32_t at = dst + (uint32_t)(q * C::RPI * KCH) * 16;
-        if constexpr (TAIL)
-          to_lds16(source(bbase, boff[q], (wave * C::NB + q) * C::RPI), at);
-        else
-          to_lds16<false>(base, boff[q], at);
-      }
+      for (int q = 0; q < C::NB; ++q) to_lds16<false>(base, boff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
     }
     ++l_kb;
   };
@@ -581,7 +583,7 @@ hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
   const int64_t a_rows = ((int64_t)p.R - 1) / p.a_div + 1;
   if (p.Kb % 128 == 0 && p.Kb / 128 >= S - 1 && a_rows * p.Kb <= ((int64_t)1 << 32))
     return ring_run<I8, F32, EPI, NT, false, BM, BN, WM, WN, S>(p, st);
-  return ring_run<I8, F32, EPI, false, true, BM, BN, WM, WN, S>(p, st);
+  return ring_run<I8, F32, EPI, NT, true, BM, BN, WM, WN, S>(p, st);
 }
 
 // The tile of a launch: the one whose rounds over the 256 CUs take the least time.  A round's cost is the time of a
