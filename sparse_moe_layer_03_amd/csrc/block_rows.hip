@@ -1,23 +1,30 @@
 // Row operators around the layer: the norms at a block's boundary with gate and residual scale, and rows of
 // 8-bit integers with one scale per row.
 //
-// All three kernels are bound by the bytes of their rows: a row is read once with 16-byte loads, held in
-// registers as long as its sums need it, and written once.  A row of up to 2048 elements belongs to one wave
-// (four rows per workgroup, no barrier), a longer one to the four waves of a workgroup, whose partial sums meet
-// in LDS.  Sums run over a lane's chunks in order and then over the lanes in a fixed tree, so results do not
+// All three kernels are bound by the bytes of their rows: a row is read once with 16-byte loads, held in registers as
+// long as its sums need it, and written once.  A row has as many waves as let a lane hold one 16-byte chunk of it (up
+// to 16 waves; rows of up to 512 elements go four to a workgroup): fewer, fuller waves took longer in every norm, the
+// weights' loads waiting behind the reductions (one token of 2048 3.8 -> 2.7 us, 8192 tokens 31.1 -> 26.7, 3000 rows of
+// 16384 139 -> 83).  Now, with a copy of 1 GiB at 4.8 TB/s: norm behind, gate, add, norm before, 8192 x 2048 26.7 us
+// (5.0 TB/s); fp32 stream with a gate per token, 1021 x 4096 11.9 (4.9); quantise 8192 x 4096 20.5 (4.9); SwiGLU rows
+// 65536 x 512 30.8 (5.4).
+//
+// Sums run over a lane's chunks in order, then over the lanes in a fixed tree and the waves in order, so results do not
 // depend on scheduling.
 //
 // Quantisation of a row: a = max(max |x|, 2^-100), scale = a / 127, code = rint(x (127 / a)), so that
-// |x - scale * code| <= scale / 2 up to fp32 rounding and no code leaves [-127, 127].  The floor on a keeps both factors normal
-// floats; rows below it become zero codes.  The maximum is taken on the magnitudes' bit patterns (ordered as the
-// magnitudes are, Inf and NaN above all finite ones): a row holding one of these gets scale NaN and zero codes,
-// and every product with it is NaN.
+// |x - scale * code| <= scale / 2 up to fp32 rounding and no code leaves [-127, 127].  The floor on a keeps both
+// factors normal floats; rows below it become zero codes.  The maximum is taken on the magnitudes' bit patterns
+// (ordered as the magnitudes are, Inf and NaN above all finite ones): a row holding one of these gets scale NaN and
+// zero codes, and every product with it is NaN.
 #include "block_internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kRowThreads = 256;
+// Threads of a workgroup whose rows have WPR waves each: four rows of one wave, else one row.
+template <int WPR>
+constexpr int kRowThreads = WPR == 1 ? 256 : 64 * WPR;
 
 // A launch holds fewer than 2^32 threads per grid dimension: workgroups beyond 2^20 go to the second one.
 dim3 row_grid(int64_t blocks) {
@@ -43,7 +50,9 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = (part[0] + part[1]) + (part[2] + part[3]);
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) v += part[w];
   }
   return v;
 }
@@ -53,7 +62,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
   if constexpr (WPR > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = max(max(part[0], part[1]), max(part[2], part[3]));
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) v = max(v, part[w]);
   }
   return v;
 }
@@ -92,12 +102,12 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
 
 // A row's chunks of 8 elements: chunk c of lane l is WPR * 64 * c + l.
 template <int CPL, int WPR, bool F32, bool YIN>
-__global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
-  __shared__ float part_y[4], part_r[4];
-  __shared__ uint32_t part_q[4];
+__global__ __launch_bounds__(kRowThreads<WPR>) void block_norm_kernel(NormArgs p) {
+  __shared__ float part_y[WPR], part_r[WPR];
+  __shared__ uint32_t part_q[WPR];
   constexpr int LANES = 64 * WPR;
   const int lane = threadIdx.x % LANES;
-  const int64_t t = block_index() * (kRowThreads / LANES) + threadIdx.x / LANES;
+  const int64_t t = block_index() * (kRowThreads<WPR> / LANES) + threadIdx.x / LANES;
   if (t >= p.T) return;
   const int nch = p.H / 8;
   const float n_inv = 1.0f / (float)p.H;
@@ -125,6 +135,15 @@ __global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
                        : reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.r) + row)[ch];
     }
   }
+  // the weights and the gate are read here too, not behind the reductions they follow
+  u32x4 pw[CPL], gw[CPL], nw[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    const int ch = min(c * LANES + lane, nch - 1);
+    if (YIN && p.w_post) pw[c] = reinterpret_cast<const u32x4*>(p.w_post)[ch];
+    if (YIN && p.gate) gw[c] = reinterpret_cast<const u32x4*>(p.gate + t * p.gate_ld)[ch];
+    if (p.w_pre) nw[c] = reinterpret_cast<const u32x4*>(p.w_pre)[ch];
+  }
   float ys = p.y_scale;
   if (YIN && p.w_post) {
     float s = 0.0f;
@@ -138,7 +157,7 @@ __global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
       const int ch = c * LANES + lane;
       if (ch < nch) {
         float w[8];
-        chunk_to_f32(reinterpret_cast<const u32x4*>(p.w_post)[ch], w);
+        chunk_to_f32(pw[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rs * (w[i] + p.w_add);
       }
@@ -160,7 +179,7 @@ __global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = ys;
       if (p.gate && ch < nch) {
-        chunk_to_f32(reinterpret_cast<const u32x4*>(p.gate + t * p.gate_ld)[ch], g);
+        chunk_to_f32(gw[c], g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] *= ys;
       }
@@ -193,7 +212,7 @@ __global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
     const int ch = c * LANES + lane;
     if (ch < nch) {
       float w[8];
-      chunk_to_f32(reinterpret_cast<const u32x4*>(p.w_pre)[ch], w);
+      chunk_to_f32(nw[c], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[c][i] = v[c][i] * rs * (w[i] + p.w_add);
@@ -214,12 +233,12 @@ __global__ __launch_bounds__(kRowThreads) void block_norm_kernel(NormArgs p) {
 
 // Rows of bf16 (SWIGLU: silu(gate) * up of rows [gate | up]) to codes and a scale per row.
 template <int CPL, int WPR, bool SWIGLU>
-__global__ __launch_bounds__(kRowThreads) void quantize_kernel(const uint16_t* x, const float* row_gate, int R, int K,
-                                                               int8_t* q, float* scale) {
-  __shared__ uint32_t part_q[4];
+__global__ __launch_bounds__(kRowThreads<WPR>) void quantize_kernel(const uint16_t* x, const float* row_gate, int R,
+                                                                    int K, int8_t* q, float* scale) {
+  __shared__ uint32_t part_q[WPR];
   constexpr int LANES = 64 * WPR;
   const int lane = threadIdx.x % LANES;
-  const int64_t t = block_index() * (kRowThreads / LANES) + threadIdx.x / LANES;
+  const int64_t t = block_index() * (kRowThreads<WPR> / LANES) + threadIdx.x / LANES;
   if (t >= R) return;
   const int nch = K / 8;
   const uint16_t* src = x + t * K * (SWIGLU ? 2 : 1);
@@ -256,45 +275,51 @@ __global__ __launch_bounds__(kRowThreads) void quantize_kernel(const uint16_t* x
   if (lane == 0) scale[t] = SWIGLU && row_gate ? sc.scale * row_gate[t] : sc.scale;
 }
 
+template <int CPL, int WPR, bool F32, bool YIN>
+void norm_run(const NormArgs& a, hipStream_t st) {
+  block_norm_kernel<CPL, WPR, F32, YIN>
+      <<<row_grid(WPR == 1 ? ((int64_t)a.T + 3) / 4 : a.T), kRowThreads<WPR>, 0, st>>>(a);
+}
 template <bool F32, bool YIN>
 void norm_launch(const NormArgs& a, hipStream_t st) {
   const int nch = a.H / 8;
-  const dim3 b1 = row_grid(((int64_t)a.T + 3) / 4), b4 = row_grid(a.T);
   if (nch <= 64)
-    block_norm_kernel<1, 1, F32, YIN><<<b1, kRowThreads, 0, st>>>(a);
+    norm_run<1, 1, F32, YIN>(a, st);
   else if (nch <= 128)
-    block_norm_kernel<2, 1, F32, YIN><<<b1, kRowThreads, 0, st>>>(a);
+    norm_run<1, 2, F32, YIN>(a, st);
   else if (nch <= 256)
-    block_norm_kernel<4, 1, F32, YIN><<<b1, kRowThreads, 0, st>>>(a);
+    norm_run<1, 4, F32, YIN>(a, st);
   else if (nch <= 512)
-    block_norm_kernel<2, 4, F32, YIN><<<b4, kRowThreads, 0, st>>>(a);
+    norm_run<1, 8, F32, YIN>(a, st);
   else if (nch <= 1024)
-    block_norm_kernel<4, 4, F32, YIN><<<b4, kRowThreads, 0, st>>>(a);
+    norm_run<1, 16, F32, YIN>(a, st);
   else
-    block_norm_kernel<8, 4, F32, YIN><<<b4, kRowThreads, 0, st>>>(a);
+    norm_run<2, 16, F32, YIN>(a, st);
 }
 
+template <int CPL, int WPR, bool SWIGLU>
+void quantize_run(const uint16_t* x, const float* row_gate, int R, int K, int8_t* q, float* scale, hipStream_t st) {
+  quantize_kernel<CPL, WPR, SWIGLU>
+      <<<row_grid(WPR == 1 ? ((int64_t)R + 3) / 4 : R), kRowThreads<WPR>, 0, st>>>(x, row_gate, R, K, q, scale);
+}
 template <bool SWIGLU>
 hipError_t quantize_launch(const uint16_t* x, const float* row_gate, int R, int K, int8_t* q, float* scale,
                            hipStream_t st) {
   const int nch = K / 8;
-  const dim3 b1 = row_grid(((int64_t)R + 3) / 4), b4 = row_grid(R);
-#define MOE_QUANT(CPL, WPR, B) quantize_kernel<CPL, WPR, SWIGLU><<<B, kRowThreads, 0, st>>>(x, row_gate, R, K, q, scale)
   if (nch <= 64)
-    MOE_QUANT(1, 1, b1);
+    quantize_run<1, 1, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else if (nch <= 128)
-    MOE_QUANT(2, 1, b1);
+    quantize_run<1, 2, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else if (nch <= 256)
-    MOE_QUANT(4, 1, b1);
+    quantize_run<1, 4, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else if (nch <= 512)
-    MOE_QUANT(2, 4, b4);
+    quantize_run<1, 8, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else if (nch <= 1024)
-    MOE_QUANT(4, 4, b4);
+    quantize_run<1, 16, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else if (nch <= 2048)
-    MOE_QUANT(8, 4, b4);
+    quantize_run<2, 16, SWIGLU>(x, row_gate, R, K, q, scale, st);
   else
-    MOE_QUANT(16, 4, b4);
-#undef MOE_QUANT
+    quantize_run<4, 16, SWIGLU>(x, row_gate, R, K, q, scale, st);
   return hipGetLastError();
 }
 

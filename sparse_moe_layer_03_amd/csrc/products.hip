@@ -147,7 +147,8 @@ __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRow
 // ---------------------------------------------------------------------------------------------------------------
 // Few rows (dense 8-bit products): a workgroup owns 16 columns and reads their weights once, straight into
 // registers.  Its four waves take every fourth 128-byte line of the rows (two 16 x 16 matrix instructions deep), U
-// lines at a time, and add their partial sums through LDS.
+// lines at a time, and add their partial sums through LDS.  One row by 2048 x 4096 takes 3.2 us, a launch and one round
+// of loads; the bytes alone would take 1.8.
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -218,8 +219,20 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// Persistent kernel: BM x BN tiles, operands loaded straight into an S-stage ring in LDS, K steps of KCH 16-byte
-// chunks per row, loads S - 1 steps ahead also across items.
+// Persistent kernel: BM x BN tiles, operands loaded straight into an S-stage ring in LDS, loads S - 1 steps ahead also
+// across items, one barrier per K step.
+//
+// What bounds it: dense 8-bit 8192 x 4096 x 4096 takes 124 us (2.2 POP/s; a library's product 131 us); with the matrix
+// instructions taken out of a copy 98 us, with the loads taken out 95 us, with loads and LDS reads out 74 us: the parts
+// overlap to within a quarter.  Grouped bf16 gate/up rows of 8192 tokens (256 experts, top-8, most of them small) take
+// 370 us, 345 without the matrix instructions: 1.6 to 1.9 GB pass the L2 caches at the 5.2 TB/s that all CUs together
+// draw from beyond them (a direct-to-LDS load from L2 alone reaches 127 GB/s per CU).  Below a mean of about 64 rows
+// per expert the weights' stream is all: 32 tokens 59 us, 5.3 TB/s.
+//
+// Measured and not taken, dense / grouped in us against 128 / 390: four waves of 128 x 128 (spills) 143 / 457; loads
+// spread between the matrix instructions 134 / 425; the last sub-step's instructions behind the barrier 131 / 404;
+// items dealt cyclically over the XCDs (even, but fewer L2 hits) - / 407; small tiles on a deeper ring of their own - /
+// 414; skipping the loads of padding rows 133 / 410.
 
 // 16 (4) bytes per lane from src to LDS at lds_base + 16 (4) * lane; lds_base is wave-uniform.  Inline assembly, so
 // that the compiler's wait counts do not order LDS reads behind loads in flight; the K loop waits itself.
@@ -230,7 +243,7 @@ __device__ __forceinline__ void to_lds4(const void* src, uint32_t lds_base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(src) : "memory");
 }
 // The K loop's form: a wave-uniform base and 32-bit lane offsets that stay the same from step to step, so that a load
-// costs no vector instruction (dense 8-bit 8192 x 4096 x 4096 128 -> 120 us, grouped bf16 prefill 394 -> 373 us).
+// costs no vector instruction (dense 8-bit 8192 x 4096 x 4096 132 -> 124 us, grouped bf16 prefill 394 -> 376 us).
 // NT: past the caches.
 template <bool NT>
 __device__ __forceinline__ void to_lds16(const char* base, uint32_t off, uint32_t lds_base) {
@@ -246,11 +259,12 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// 16-byte chunk swizzle of an LDS row of KCH chunks, the XOR term for a row (rows repeat every 16).
-template <int KCH>
-__device__ __forceinline__ int swz_term(int row) {
-  return KCH == 8 ? (((row >> 1) ^ ((row & 1) << 2)) & 7) : (((row >> 1) ^ (row >> 2)) & 3);
-}
+// A K step is 128 bytes of a row, 8 chunks of 16.  (64-byte steps in twice the stages read every cache line in two
+// halves: dense 8-bit 8192 x 4096 x 4096 145 -> 157 us.)
+constexpr int kCh = 8;
+// In LDS chunk c of a row lies at c ^ swz_term(row): any 16 consecutive rows read at one chunk hit 16 distinct bank
+// groups.
+__device__ __forceinline__ int swz_term(int row) { return ((row >> 1) ^ ((row & 1) << 2)) & 7; }
 
 // Row tiles of an expert whose items run together over all column blocks, so that the 32 workgroups of an XCD read
 // few distinct rows and columns at a time.
@@ -281,7 +295,9 @@ struct ProductList {
       first[i] = count[i] = 0;
       if (e < p.E) expert_range(p, e, first[i], count[i]);
       start[i] = sum;
-      sum += ((count[i] + BM - 1) / BM) * nbn;
+      // the bound, beyond any product that fits the memory, keeps 256 counts in an int whatever off and counts hold
+      const int64_t items = (int64_t)((count[i] + BM - 1) / BM) * nbn;
+      sum += (int)(items < (1 << 23) ? items : (1 << 23) - 1);
     }
     int incl = sum;
 #pragma unroll
@@ -299,11 +315,10 @@ struct ProductList {
     int j = item, rows = p.P, base = 0;
     it.expert = 0;
     if (p.off) {
-      // experts that start at or before the item; the last of them holds it (empty ones start where the next does)
+      // of the experts that start at or before the item the last one holds it: an empty one starts where the next does
       int n = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) n += __popcll(__ballot(start[i] <= item));
-      // several experts may start here: the empty ones among them precede the one that holds the item
       it.expert = min(n, p.E) - 1;
       const int l = it.expert >> 2, q = it.expert & 3;
       const int f = q == 0 ? first[0] : q == 1 ? first[1] : q == 2 ? first[2] : first[3];
@@ -326,22 +341,23 @@ struct ProductList {
   }
 };
 
-template <bool I8, bool EPI, int BM, int BN, int WM, int WN, int KCH, int S>
+template <bool I8, bool EPI, int BM, int BN, int WM, int WN, int S>
 struct RingCfg {
   static constexpr int NW = WM * WN, NT = NW * 64, MI = BM / WM / 32, NJ = BN / WN / 32;
-  static constexpr int RPI = 64 / KCH;  // rows one load instruction fills
+  static constexpr int RPI = 64 / kCh;  // rows one load instruction fills
   static constexpr int NA = BM / RPI / NW, NB = BN / RPI / NW;  // load instructions per wave and step
-  static constexpr int STAGE = (BM + BN) * KCH;  // chunks
-  static constexpr int SUB = KCH / 2;  // matrix instructions deep per step
+  static constexpr int STAGE = (BM + BN) * kCh;  // chunks
+  static constexpr int SUB = kCh / 2;  // matrix instructions deep per step
   // LDS: stages, output rows of three items, scales and biases of two items
-  static constexpr size_t LDS = (size_t)S * STAGE * 16 + 3 * BM * 4 + (I8 ? 2 * (BM + BN) * 4 : 0) + (EPI ? 2 * BN * 4 : 0);
+  static constexpr size_t LDS =
+      (size_t)S * STAGE * 16 + 3 * BM * 4 + (I8 ? 2 * (BM + BN) * 4 : 0) + (EPI ? 2 * BN * 4 : 0);
   static constexpr int PER_CU = LDS * 2 <= 160 * 1024 ? 2 : 1;
   static_assert(BM % (RPI * NW) == 0 && BN % (RPI * NW) == 0 && BN <= NT && BM <= NT && LDS <= 160 * 1024, "");
 };
 
-template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int KCH, int S>
+template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
-  using C = RingCfg<I8, EPI, BM, BN, WM, WN, KCH, S>;
+  using C = RingCfg<I8, EPI, BM, BN, WM, WN, S>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -364,13 +380,14 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   float* s_sb = s_sa + 2 * BM;                                           // [2][BN]
   float* s_bias = s_sb + 2 * BN;                                         // [2][BN]
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  const uint32_t lds_ids = lds0 + S * C::STAGE * 16, lds_sa = lds_ids + 3 * BM * 4, lds_sb = lds_sa + 2 * BM * 4, lds_bias = lds_sb + 2 * BN * 4;
+  const uint32_t lds_ids = lds0 + S * C::STAGE * 16, lds_sa = lds_ids + 3 * BM * 4;
+  const uint32_t lds_sb = lds_sa + 2 * BM * 4, lds_bias = lds_sb + 2 * BN * 4;
 
   // at least S - 1 steps per item (those behind the row's end read zeros), so that an item's row ids have landed
   // when its loads begin and no buffer of an item is refilled before its epilogue
-  const int nk = max((p.Kb + KCH * 16 - 1) / (KCH * 16), S - 1);
+  const int nk = max((p.Kb + kCh * 16 - 1) / (kCh * 16), S - 1);
   // TAIL: steps without a row's end in them, and whether every A offset fits 32 bits
-  const int full = p.Kb / (KCH * 16);
+  const int full = p.Kb / (kCh * 16);
   const bool narrow = !TAIL || ((uint64_t)a_row(p, p.R - 1) + 1) * p.Kb <= (1ull << 32);
 
   // ---- loads
@@ -378,15 +395,16 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   ProductItem nit = list.at(p, begin);  // the one after it
   int l_index = -1, l_kb = nk;
   // byte offsets of this lane's rows from A and from the item's first B row
-  std::conditional_t<TAIL, uint64_t, uint32_t> aoff[C::NA];
+  typedef std::conditional_t<TAIL, uint64_t, uint32_t> aoff_t;
+  aoff_t aoff[C::NA];
   uint32_t boff[C::NB];
   const char* abase = static_cast<const char*>(p.a);
   const char* bbase = abase;
-  const int lrow = lane / KCH;  // row of this lane within a load instruction
-  auto chunk = [&](int r) { return (lane % KCH) ^ swz_term<KCH>(r); };  // logical chunk this lane fetches of row r
+  const int lrow = lane / kCh;  // row of this lane within a load instruction
+  auto chunk = [&](int r) { return (lane % kCh) ^ swz_term(r); };  // logical chunk this lane fetches of row r
   // this lane's 16 bytes at off, or zeros where they lie behind the row's end; r: the load's first tile row
   auto source = [&](const char* base, uint64_t off, int r) {
-    const int k = l_kb * (KCH * 16);
+    const int k = l_kb * (kCh * 16);
     return k + chunk(r + lrow) * 16 < p.Kb ? base + off + k : reinterpret_cast<const char*>(kZeros);
   };
   auto load_ids = [&](int index, const ProductItem& it) {
@@ -411,7 +429,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
     for (int q = 0; q < C::NA; ++q) {
       const int r = (wave * C::NA + q) * C::RPI + lrow;
       const int id = max(row_id(l_index, lit, r), 0);  // rows without data read row 0
-      aoff[q] = (decltype(aoff[q] + 0))((uint64_t)a_row(p, id) * p.Kb + chunk(r) * 16);
+      aoff[q] = (aoff_t)((uint64_t)a_row(p, id) * p.Kb + chunk(r) * 16);
     }
     bbase = static_cast<const char*>(p.b) + ((size_t)lit.expert * p.N + lit.n0) * p.Kb;
 #pragma unroll
@@ -421,7 +439,8 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
     }
     if constexpr (I8) {
       const int par = l_index & 1, r = wave * 64 + lane;
-      if (r < BM) to_lds4(p.a_scale + a_row(p, max(row_id(l_index, lit, r), 0)), lds_sa + (uint32_t)(par * BM + wave * 64) * 4);
+      if (r < BM)
+        to_lds4(p.a_scale + a_row(p, max(row_id(l_index, lit, r), 0)), lds_sa + (uint32_t)(par * BM + wave * 64) * 4);
       if (r < BN)
         to_lds4(p.b_scale + (size_t)lit.expert * p.N + min(lit.n0 + r, p.N - 1),
                 lds_sb + (uint32_t)(par * BN + wave * 64) * 4);
@@ -432,31 +451,31 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   };
   // The loads of one operand of a step.  Behind the last item they repeat its last step (TAIL: read zeros).
   auto issue_a = [&](int slot) {
-    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * KCH) * 16;
-    const char* base = abase + min(l_kb, nk - 1) * (KCH * 16);
+    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)(wave * C::NA * C::RPI * kCh) * 16;
+    const char* base = abase + min(l_kb, nk - 1) * (kCh * 16);
     if (TAIL && (l_kb >= full || !narrow)) {
 #pragma unroll
       for (int q = 0; q < C::NA; ++q)
-        to_lds16(source(abase, aoff[q], (wave * C::NA + q) * C::RPI), dst + (uint32_t)(q * C::RPI * KCH) * 16);
+        to_lds16(source(abase, aoff[q], (wave * C::NA + q) * C::RPI), dst + (uint32_t)(q * C::RPI * kCh) * 16);
     } else {
 #pragma unroll
       for (int q = 0; q < C::NA; ++q)
-        to_lds16<false>(base, (uint32_t)aoff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
+        to_lds16<false>(base, (uint32_t)aoff[q], dst + (uint32_t)(q * C::RPI * kCh) * 16);
     }
   };
   auto issue_b = [&](int slot) {
-    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * KCH) * 16;
-    const char* base = bbase + min(l_kb, nk - 1) * (KCH * 16);
+    const uint32_t dst = lds0 + (uint32_t)slot * (C::STAGE * 16) + (uint32_t)((BM + wave * C::NB * C::RPI) * kCh) * 16;
+    const char* base = bbase + min(l_kb, nk - 1) * (kCh * 16);
     if (TAIL && l_kb >= full) {
 #pragma unroll
       for (int q = 0; q < C::NB; ++q)
-        to_lds16(source(bbase, boff[q], (wave * C::NB + q) * C::RPI), dst + (uint32_t)(q * C::RPI * KCH) * 16);
+        to_lds16(source(bbase, boff[q], (wave * C::NB + q) * C::RPI), dst + (uint32_t)(q * C::RPI * kCh) * 16);
     } else if (NT && lit.only) {
 #pragma unroll
-      for (int q = 0; q < C::NB; ++q) to_lds16<true>(base, boff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
+      for (int q = 0; q < C::NB; ++q) to_lds16<true>(base, boff[q], dst + (uint32_t)(q * C::RPI * kCh) * 16);
     } else {
 #pragma unroll
-      for (int q = 0; q < C::NB; ++q) to_lds16<false>(base, boff[q], dst + (uint32_t)(q * C::RPI * KCH) * 16);
+      for (int q = 0; q < C::NB; ++q) to_lds16<false>(base, boff[q], dst + (uint32_t)(q * C::RPI * kCh) * 16);
     }
     ++l_kb;
   };
@@ -468,11 +487,11 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
     u32x4 a[C::MI], b[C::NJ];
   };
   auto read_frags = [&](Frag& f, const u32x4* st, int sub) {
-    const int c = frow * KCH + ((2 * sub + (lane >> 5)) ^ swz_term<KCH>(frow));
+    const int c = frow * kCh + ((2 * sub + (lane >> 5)) ^ swz_term(frow));
 #pragma unroll
-    for (int m = 0; m < C::MI; ++m) f.a[m] = st[(m * WM + wm) * 32 * KCH + c];
+    for (int m = 0; m < C::MI; ++m) f.a[m] = st[(m * WM + wm) * 32 * kCh + c];
 #pragma unroll
-    for (int j = 0; j < C::NJ; ++j) f.b[j] = st[(BM + (wn * C::NJ + j) * 32) * KCH + c];
+    for (int j = 0; j < C::NJ; ++j) f.b[j] = st[(BM + (wn * C::NJ + j) * 32) * kCh + c];
   };
 
   // ---- start: the first item's row ids, then S - 1 steps of loads
@@ -558,8 +577,8 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
 
 template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
 hipError_t ring_run(const ProductArgs& p, hipStream_t st) {
-  using C = RingCfg<I8, EPI, BM, BN, WM, WN, 8, S>;
-  const auto kernel = ring_kernel<I8, F32, EPI, NT, TAIL, BM, BN, WM, WN, 8, S>;
+  using C = RingCfg<I8, EPI, BM, BN, WM, WN, S>;
+  const auto kernel = ring_kernel<I8, F32, EPI, NT, TAIL, BM, BN, WM, WN, S>;
   // more than 64 KB of LDS has to be allowed once per device
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
@@ -577,7 +596,7 @@ hipError_t ring_run(const ProductArgs& p, hipStream_t st) {
 }
 
 // Rows that are whole steps, of which there are enough to fill the ring, and A offsets of 32 bits take the form
-// without tail handling.
+// without tail handling (grouped bf16 prefill 367 against 375 us with it).
 template <bool I8, bool F32, bool EPI, bool NT, int BM, int BN, int WM, int WN, int S>
 hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
   const int64_t a_rows = ((int64_t)p.R - 1) / p.a_div + 1;
@@ -586,26 +605,28 @@ hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
   return ring_run<I8, F32, EPI, NT, true, BM, BN, WM, WN, S>(p, st);
 }
 
-// The tile of a launch: the one whose rounds over the 256 CUs take the least time.  A round's cost is the time of a
-// 128-byte K step in us, measured with all CUs busy (dense 8-bit, 8192 x 4096 x 4096: 128, 153, 195 and 328 us);
-// the 80 KB tiles run two to a CU, their cost is half a pair's.  Grouped launches count half a tile of padding per
-// expert.  Per tile 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128:
-//   dense 8-bit, K 2048: 300 x 1024 27 / 18 / 9.5 / 7.9 us, 512 x 4096 28 / 18 / 10.9 / 14.9, 2048 x 2048
-//   29 / 19.6 / 17.4 / 26, 4096 x 4096 42 / 46 / 56 / 90
-//   bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 101 / 79 / 74 / 68 us, 512 tokens 168 / 146 / 146 / 145,
-//   2048 tokens 222 / 199 / 216 / 268, 8192 tokens 390 / 397 / 497 / 763
+// The tile of a launch: the one whose rounds over the 256 CUs take the least time, rounds counted whole up to two of
+// them.  A round's cost is a 128-byte K step's time in us with all CUs busy (dense 8-bit, 8192 x 4096 x 4096: 120, 137,
+// 178 and 287 us; 64 x 128 tiles run two to a CU and count half a pair's time), raised by a quarter for the two small
+// tiles, which read the same rows more often than a grouped launch's weight streams leave room for.  Grouped launches
+// count half a tile of padding per expert.  Measured, us, tiles of 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128:
+//   dense 8-bit, K 2048: 300 x 1024 25 / 16 / 8.3 / 7.0, 512 x 4096 26 / 17 / 9.9 / 13, 2048 x 2048 27 / 18 / 15.5 /
+//   23, 4096 x 4096 39 / 42 / 51 / 78
+//   bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 91 / 73 / 65 / 59, 512 tokens 163 / 136 / 133 / 142, 1024
+//   tokens 171 / 159 / 168 / 186, 2048 tokens 215 / 196 / 213 / 259, 8192 tokens 374 / 371 / 484 / 710
 template <bool I8, bool F32, bool EPI, bool NT>
 hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
   static const struct {
     int bm, bn;
     float cost;
-  } tiles[] = {{256, 256, 1.95f}, {128, 256, 1.2f}, {64, 128, 0.46f}, {32, 128, 0.37f}};
+  } tiles[] = {{256, 256, 1.8f}, {128, 256, 1.1f}, {64, 128, 0.43f}, {32, 128, 0.36f}};
   int best = 0;
   float least = 0.0f;
   for (int i = 0; i < 4; ++i) {
-    const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1 : (p.P + tiles[i].bm - 1) / tiles[i].bm;
+    const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1
+                               : ((int64_t)p.P + tiles[i].bm - 1) / tiles[i].bm;
     const int64_t items = rows * ((p.N + tiles[i].bn - 1) / tiles[i].bn);
-    const float rounds = items <= 1024 ? (float)((items + 255) / 256) : (float)items / 256.0f;
+    const float rounds = items <= 512 ? (float)((items + 255) / 256) : (float)items / 256.0f;
     const float t = rounds * tiles[i].cost;
     if (i == 0 || t < least) best = i, least = t;
   }
@@ -619,14 +640,15 @@ hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
 
 template <bool F32, bool EPI>
 hipError_t dense_i8_launch(const ProductArgs& p, hipStream_t st) {
-  // up to 64 rows: us of the few-rows kernel (one / four row blocks) against the best tile, K 2048: 1 x 4096 3.5 /
-  // 4.6 against 7.2, 33 x 1024 - / 5.8 against 7.5, 64 x 4096 - / 7.3 against 7.7
+  // The few-rows kernel against the best tile, us (rows x K x columns): 1 x 2048 x 4096 3.2 against 7.2; 33 x 512 x
+  // 4096 3.4 against 4.3, 64 x 1024 x 1024 4.3 against 5.0, 64 x 2048 x 4096 6.9 against 7.0, 64 x 4096 x 4096 13.5
+  // against 10.4 (every workgroup reads all rows of A, and its loads come in batches).  256 workgroups fill the CUs.
   const unsigned blocks = (unsigned)((p.N + 15) / 16);
   if (p.P <= 16) {
     skinny_kernel<F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }
-  if (p.P <= 64 && blocks <= 256) {
+  if (p.P <= 64 && p.Kb <= 2048 && blocks <= 256) {
     skinny_kernel<F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }

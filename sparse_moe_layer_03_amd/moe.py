@@ -321,17 +321,18 @@ def _args(*tensors):
     Refuses what the C ABI cannot tell from the right tensor: another type, too few elements, strides, or another
     device than the current one (whose stream the call is enqueued on)."""
     out = []
-    at = set()
+    dev = None
     for name, t, dtype, numel in tensors:
         if t is None or t.__class__ is int:
             out.append(t)
-        elif t.dtype is dtype and t.numel() >= numel and t.is_contiguous() and t.is_cuda:
+        elif t.dtype is dtype and t.numel() >= numel and t.is_contiguous() and (at := t.get_device()) >= 0:
+            if at != dev:
+                dev = _device()
+                if at != dev:
+                    raise ValueError(f"{name} is on GPU {at}; the current one is {dev}")
             out.append(t.data_ptr())
-            at.add(t.get_device())
         else:
             raise ValueError(_fault(name, t, dtype, numel))
-    if at and at != {_device()}:
-        raise ValueError(f"tensors on GPU {sorted(at)}; the current one is {_device()}")
     return out
 
 

@@ -223,7 +223,8 @@ def test_products_over_align(torch, T):
     rows = moe.moe_align_max_rows(T, E, k)
     i32 = dict(dtype=torch.int32, device="cuda")
     counts, off, srt = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(rows, **i32)
-    inv, tiles, nt = torch.empty(n, **i32), torch.empty(2 * moe.moe_align_max_tiles(T, E, k), **i32), torch.empty(2, **i32)
+    inv, nt = torch.empty(n, **i32), torch.empty(2, **i32)
+    tiles = torch.empty(2 * moe.moe_align_max_tiles(T, E, k), **i32)
     scratch = torch.empty(moe.moe_align_scratch_size(T, E, k), dtype=torch.uint8, device="cuda")
     moe.moe_align(ids, T, E, k, counts, off, srt, inv, tiles, nt, scratch, scratch.numel())
     flat = ids.reshape(-1).long()

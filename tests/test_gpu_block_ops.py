@@ -175,7 +175,8 @@ DENSE = [(1, 8, 16), (1, 4096, 2048), (2, 24, 48), (3, 1000, 112), (15, 72, 128)
          (31, 512, 2048), (33, 1024, 1040), (48, 40, 4096), (63, 2048, 512), (64, 256, 64), (65, 264, 4112),
          (100, 8, 8192), (127, 520, 272), (128, 128, 2048), (129, 1032, 384), (200, 2048, 2048), (255, 256, 128),
          (256, 512, 1024), (257, 768, 640), (300, 1544, 784), (511, 24, 16), (1000, 1000, 1008), (1024, 2048, 2048),
-         (2049, 520, 528), (70, 40, 65536)]
+         (2049, 520, 528), (70, 40, 65536), (2000, 3000, 400), (2001, 3000, 384), (3900, 4104, 272), (4096, 4096, 256),
+         (64, 4096, 2048), (65, 4104, 2064), (40, 4096, 1024), (17, 8200, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -205,7 +206,8 @@ def test_gemm_i8_largest_sum(torch):
     assert bool((c == -128.0 * 127 * K).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 264, 512), (20, 72, 2064), (50, 1024, 256), (130, 520, 1024), (600, 776, 528)])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 512), (20, 72, 2064), (50, 1024, 256), (130, 520, 1024), (600, 776, 528),
+                                   (2000, 3000, 400), (3900, 4104, 272)])
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 @pytest.mark.parametrize("bias,add", [(False, False), (True, False), (False, True), (True, True)])
 def test_gemm_i8_epilogue(torch, M, N, K, out, bias, add):
@@ -266,9 +268,12 @@ def layout(torch, g, kind, E, T, k):
 GROUPED = [("random", 1, 3, 1, 16, 32), ("random", 4, 50, 2, 72, 112), ("contiguous", 8, 77, 3, 264, 144),
            ("padded", 16, 60, 4, 128, 528), ("one expert", 5, 300, 1, 520, 256), ("few", 60, 37, 8, 1416, 1008),
            ("random", 256, 4, 8, 1024, 2048), ("random", 256, 32, 8, 136, 2048), ("padded", 64, 500, 6, 512, 512),
-           ("random", 128, 640, 8, 256, 272), ("contiguous", 3, 1000, 2, 328, 784), ("one expert", 256, 700, 2, 264, 128),
+           ("random", 128, 640, 8, 256, 272), ("contiguous", 3, 1000, 2, 328, 784),
+           ("one expert", 256, 700, 2, 264, 128),
            ("random", 256, 2100, 8, 512, 128), ("few", 256, 513, 16, 1032, 64), ("contiguous", 256, 1, 1, 8, 16),
-           ("random", 32, 2000, 4, 2048, 512), ("padded", 256, 300, 8, 72, 16)]
+           ("random", 32, 2000, 4, 2048, 512), ("padded", 256, 300, 8, 72, 16),
+           # the largest tiles: rows that are whole steps and rows that are not
+           ("random", 16, 9000, 2, 2048, 256), ("padded", 10, 9001, 2, 2056, 144)]
 
 
 @pytest.mark.parametrize("kind,E,T,k,N,K", GROUPED)
@@ -355,6 +360,25 @@ def test_grouped_offsets_out_of_range_are_clipped(torch):
         moe.moe_grouped_gemm(a, b, off, counts, None, 1, P, P, E, N, K, c)
         torch.cuda.synchronize()
         assert bool(((c == 0) | (c == K)).all()) and bool((c[P:] == 0).all())
+
+
+@pytest.mark.parametrize("rows_of_a", [140_000, 270_000])
+def test_large_a_offsets(torch, rows_of_a):
+    """A rows beyond 2^31 and beyond 2^32 bytes, gathered and in order."""
+    K, N, E, P = 16384, 64, 3, 300
+    g = B.gen(rows_of_a)
+    a = torch.zeros(rows_of_a, K, dtype=torch.int8, device="cuda")
+    a[-P:] = B.ints(g, (P, K), -9, 9, torch.int8)
+    sa, sb = torch.ones(rows_of_a, device="cuda"), torch.ones(E, N, device="cuda")
+    b = B.ints(g, (E, N, K), -9, 9, torch.int8)
+    rows = (torch.randperm(P, generator=g, device="cuda") + rows_of_a - P).int()
+    off = torch.tensor([0, 100, 101, P], dtype=torch.int32, device="cuda")
+    c = torch.zeros(rows_of_a, N, device="cuda")
+    moe.moe_grouped_gemm_i8(a, sa, b, sb, off, None, rows, 1, P, rows_of_a, E, N, K, c)
+    for e in range(E):
+        t = rows[int(off[e]):int(off[e + 1])].long()
+        assert torch.equal(c[t], (a[t].double() @ b[e].double().t()).float())
+    assert int(torch.count_nonzero(c[:-P])) == 0
 
 
 def test_large_offsets(torch):
