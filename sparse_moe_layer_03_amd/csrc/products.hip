@@ -236,14 +236,15 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
 // What bounds it: dense 8-bit 8192 x 4096 x 4096 takes 124 us (2.2 POP/s; a library's product 131 us); with the matrix
 // instructions taken out of a copy 98 us, with the loads taken out 95 us, with loads and LDS reads out 74 us: the parts
 // overlap to within a quarter.  Grouped bf16 gate/up rows of 8192 tokens (256 experts, top-8, most of them small) take
-// 370 us, 345 without the matrix instructions: 1.6 to 1.9 GB pass the L2 caches at the 5.2 TB/s that all CUs together
+// 367 us, 345 without the matrix instructions: 1.6 to 1.9 GB pass the L2 caches at the 5.2 TB/s that all CUs together
 // draw from beyond them (a direct-to-LDS load from L2 alone reaches 127 GB/s per CU).  Below a mean of about 64 rows
-// per expert the weights' stream is all: 32 tokens 59 us, 5.3 TB/s.
+// per expert the weights' stream is all: 32 tokens 55 us, 5.8 TB/s.
 //
 // Measured and not taken, dense / grouped in us against 128 / 390: four waves of 128 x 128 (spills) 143 / 457; loads
 // spread between the matrix instructions 134 / 425; the last sub-step's instructions behind the barrier 131 / 404;
 // items dealt cyclically over the XCDs (even, but fewer L2 hits) - / 407; small tiles on a deeper ring of their own - /
-// 414; skipping the loads of padding rows 133 / 410.
+// 414; skipping the loads of padding rows 133 / 410.  Leaving an item's stores in flight over the next item's first
+// steps: 123 / 374 against 122 / 372 by then (3% less with an addend, nothing elsewhere).
 
 // 16 (4) bytes per lane from src to LDS at lds_base + 16 (4) * lane; lds_base is wave-uniform.  Inline assembly, so
 // that the compiler's wait counts do not order LDS reads behind loads in flight; the K loop waits itself.
@@ -618,48 +619,56 @@ hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
 
 // The tile of a launch: the one whose rounds over the 256 CUs take the least time, rounds counted whole up to two of
 // them.  A round's cost is a 128-byte K step's time in us with all CUs busy (dense 8-bit, 8192 x 4096 x 4096: 120, 137,
-// 178 and 287 us; 64 x 128 tiles run two to a CU and count half a pair's time), raised by a quarter for the two small
-// tiles, which read the same rows more often than a grouped launch's weight streams leave room for.  Grouped launches
-// count half a tile of padding per expert.  Measured, us, tiles of 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128:
-//   dense 8-bit, K 2048: 300 x 1024 25 / 16 / 8.3 / 7.0, 512 x 4096 26 / 17 / 9.9 / 13, 2048 x 2048 27 / 18 / 15.5 /
-//   23, 4096 x 4096 39 / 42 / 51 / 78
-//   bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 91 / 73 / 65 / 59, 512 tokens 163 / 136 / 133 / 142, 1024
-//   tokens 171 / 159 / 168 / 186, 2048 tokens 215 / 196 / 213 / 259, 8192 tokens 374 / 371 / 484 / 710
+// 178 and 287 us; the tiles of 128 and fewer columns run two to a CU and count half a pair's time), raised by a quarter
+// for the small tiles, which read the same rows more often than a grouped launch's weight streams leave room for.  The
+// narrowest tile costs half of the next, a little less where long rows hide its item changes.  Grouped launches count
+// half a tile of padding per expert.  Measured, us, tiles of 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128 / 32 x 64:
+//   dense 8-bit, K 2048: 300 x 1024 25 / 16 / 8.2 / 6.6 / 6.4, 512 x 4096 26 / 17 / 9.5 / 12.5 / 14, 2048 x 2048 27 /
+//   18 / 15.8 / 22 / 25, 4096 x 4096 39 / 43 / 51 / 78 / 87
+//   bf16, 256 experts, top-8, K 2048, N 1024: 1 token (weights from HBM) - / - / 19 / 16 / 12, 32 tokens 88 / 68 / 59 /
+//   57 / 56, 512 tokens 152 / 124 / 126 / 123 / 129, 1024 tokens 161 / 151 / 162 / 176 / 187, 2048 tokens 208 / 189 /
+//   212 / 243 / 269, 8192 tokens 368 / 366 / - / - / -
+//   8-bit, K 512, N 2048: 128 tokens 36 / 29 / 27 / 26 / 28, 777 tokens 56 / 46 / 44 / 51 / 57
 template <bool I8, bool F32, bool EPI, bool NT>
 hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
-  static const struct {
+  const struct {
     int bm, bn;
     float cost;
-  } tiles[] = {{256, 256, 1.8f}, {128, 256, 1.1f}, {64, 128, 0.43f}, {32, 128, 0.36f}};
-  int best = 0;
+  } tiles[] = {
+      {256, 256, 1.8f}, {128, 256, 1.1f}, {64, 128, 0.43f}, {32, 128, 0.36f}, {32, 64, p.Kb < 2048 ? 0.19f : 0.175f}};
+  constexpr int kFirst = NT ? 1 : 0;  // below a mean of 64 rows the largest tile is never the best
+  int best = kFirst;
   float least = 0.0f;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = kFirst; i < 5; ++i) {
     const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1
                                : ((int64_t)p.P + tiles[i].bm - 1) / tiles[i].bm;
     const int64_t items = rows * ((p.N + tiles[i].bn - 1) / tiles[i].bn);
     const float rounds = items <= 512 ? (float)((items + 255) / 256) : (float)items / 256.0f;
     const float t = rounds * tiles[i].cost;
-    if (i == 0 || t < least) best = i, least = t;
+    if (i == kFirst || t < least) best = i, least = t;
   }
   switch (best) {
-    case 0: return ring_launch<I8, F32, EPI, NT, 256, 256, 4, 2, 2>(p, st);
+    case 0:
+      if constexpr (!NT) return ring_launch<I8, F32, EPI, NT, 256, 256, 4, 2, 2>(p, st);
     case 1: return ring_launch<I8, F32, EPI, NT, 128, 256, 2, 4, 3>(p, st);
     case 2: return ring_launch<I8, F32, EPI, NT, 64, 128, 2, 2, 3>(p, st);
-    default: return ring_launch<I8, F32, EPI, NT, 32, 128, 1, 4, 4>(p, st);
+    case 3: return ring_launch<I8, F32, EPI, NT, 32, 128, 1, 4, 4>(p, st);
+    default: return ring_launch<I8, F32, EPI, NT, 32, 64, 1, 2, 5>(p, st);
   }
 }
 
 template <bool F32, bool EPI>
 hipError_t dense_i8_launch(const ProductArgs& p, hipStream_t st) {
-  // The few-rows kernel against the best tile, us (rows x K x columns): 1 x 2048 x 4096 3.2 against 7.2; 33 x 512 x
-  // 4096 3.4 against 4.3, 64 x 1024 x 1024 4.3 against 5.0, 64 x 2048 x 4096 6.9 against 7.0, 64 x 4096 x 4096 13.5
-  // against 10.4 (every workgroup reads all rows of A, and its loads come in batches).  256 workgroups fill the CUs.
+  // The few-rows kernel against the best tile, us (rows x K x columns): 1 x 2048 x 4096 3.2 against 6.1, 16 rows 3.9
+  // against 6.2; 33 x 512 x 4096 3.5 against 4.0, 64 x 1024 x 4096 4.6 against 4.8, 48 x 2048 x 4096 6.2 against 6.3,
+  // 64 rows 7.3 against 6.5, 33 x 4096 x 4096 11.1 against 9.5 (every workgroup reads all rows of A, and its loads
+  // come in batches).  256 workgroups fill the CUs.
   const unsigned blocks = (unsigned)((p.N + 15) / 16);
   if (p.P <= 16) {
     skinny_kernel<F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }
-  if (p.P <= 64 && p.Kb <= 2048 && blocks <= 256) {
+  if (p.P <= 64 && p.Kb <= 2048 && p.P * p.Kb <= 48 * 2048 && blocks <= 256) {
     skinny_kernel<F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }
@@ -670,8 +679,8 @@ template <bool I8, bool F32>
 hipError_t grouped_launch(const ProductArgs& p, hipStream_t st) {
   // Below a mean of 64 rows per expert a launch mostly streams weights: where they would not stay in the 256 MB
   // Infinity Cache in any case, those of an expert's only tile pass the caches by, which then keep the rows of A and
-  // C.  With / without, bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 61 / 65 us, 512 tokens 135 / 144; at a
-  // mean of 64 200 / 199, above it slower (8192 tokens 407 / 401); 1 token, 33 MB of weights, 18.3 / 13.9 repeated
+  // C.  With / without, us, bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 54.6 / 59.2, 512 tokens 118 / 137; at
+  // a mean of 64 190 / 180, at 256 363 / 367; 1 token, 33 MB of weights, 13.4 / 11.1 repeated, 13.3 / 13.8 from HBM
   const int64_t touched = (int64_t)(p.E < p.R ? p.E : p.R) * p.N * p.Kb;
   if (p.R / p.E < 64 && touched > (128 << 20)) return tiled_launch<I8, F32, false, true>(p, st);
   return tiled_launch<I8, F32, false, false>(p, st);

@@ -313,6 +313,16 @@ def test_grouped_exact(torch, kind, E, T, k, N, K, typ, out):
     same_bits(torch, c, ref, "c")
 
 
+# every tile with rows of whole steps and without, with weights that pass the caches by and that do not
+@pytest.mark.parametrize("kind,E,T,k,N,K", [("random", 64, 900, 4, 520, 384), ("random", 256, 12, 8, 2048, 512),
+                                            ("few", 256, 16, 8, 4096, 272), ("random", 256, 32, 8, 1024, 1024),
+                                            ("padded", 256, 300, 8, 1032, 1040), ("random", 256, 500, 8, 1024, 1024),
+                                            ("random", 256, 1000, 8, 1024, 1024)])
+@pytest.mark.parametrize("typ", ["bf16", "i8"])
+def test_grouped_weight_streams(torch, kind, E, T, k, N, K, typ):
+    test_grouped_exact(torch, kind, E, T, k, N, K, typ, "bf16")
+
+
 @pytest.mark.parametrize("kind,E,T,k,N,K", [GROUPED[i] for i in (1, 5, 7, 9, 15)])
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 def test_grouped_general_values(torch, kind, E, T, k, N, K, out):
