@@ -233,12 +233,12 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
 // Persistent kernel: BM x BN tiles, operands loaded straight into an S-stage ring in LDS, loads S - 1 steps ahead also
 // across items, one barrier per K step.
 //
-// What bounds it: dense 8-bit 8192 x 4096 x 4096 takes 124 us (2.2 POP/s; a library's product 131 us); with the matrix
+// What bounds it: dense 8-bit 8192 x 4096 x 4096 takes 122 us (2.25 POP/s; a library's product 131 us); with the matrix
 // instructions taken out of a copy 98 us, with the loads taken out 95 us, with loads and LDS reads out 74 us: the parts
 // overlap to within a quarter.  Grouped bf16 gate/up rows of 8192 tokens (256 experts, top-8, most of them small) take
 // 367 us, 345 without the matrix instructions: 1.6 to 1.9 GB pass the L2 caches at the 5.2 TB/s that all CUs together
 // draw from beyond them (a direct-to-LDS load from L2 alone reaches 127 GB/s per CU).  Below a mean of about 64 rows
-// per expert the weights' stream is all: 32 tokens 55 us, 5.8 TB/s.
+// per expert the weights' stream is all: 32 tokens 53 us, 5.9 TB/s.
 //
 // Measured and not taken, dense / grouped in us against 128 / 390: four waves of 128 x 128 (spills) 143 / 457; loads
 // spread between the matrix instructions 134 / 425; the last sub-step's instructions behind the barrier 131 / 404;
