@@ -468,7 +468,8 @@ int moe_swiglu_i8(const uint16_t* gu, const float* row_gate, int R, int I, int8_
  * The sum is exact (int32); the rest is fp32, rounded once.
  *   a [M,K], b [N,K] int8 (every code, -128 included), a_scale [M], b_scale [N] fp32, bias [N] fp32 or NULL,
  *   add [M,N] bf16 or NULL (may be c itself when c is bf16), c [M,N] bf16 or fp32 (c_type).
- *   K % 16 == 0, 16 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^20; M <= 2^28.  M = 0 is a successful no-op.
+ *   K % 16 == 0, 16 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^20; M <= 2^28; M * N <= 2^37.  M = 0 is a successful
+ *   no-op.
  */
 int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, const float* bias,
                 const uint16_t* add, int M, int N, int K, void* c, int c_type, void* stream);
@@ -486,7 +487,8 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const fl
  *   moe_grouped_gemm: a, b bf16, fp32 sums, K % 8 == 0.
  *   moe_grouped_gemm_i8: a, b int8, int32 sums, times a_scale [rows of a] and b_scale [E,N] as moe_gemm_i8;
  *   K % 16 == 0.
- *   1 <= E <= 256; K <= 65536; N % 8 == 0, 8 <= N <= 2^20; P, R <= 2^28 (0: no-op); a_div >= 1.
+ *   1 <= E <= 256; K <= 65536; N % 8 == 0, 8 <= N <= 2^20; P, R <= 2^28 (0: no-op); P * N <= 2^37;
+ *   a_div >= 1.
  */
 int moe_grouped_gemm(const uint16_t* a, const uint16_t* b, const int32_t* off, const int32_t* counts,
                      const int32_t* rows, int a_div, int P, int R, int E, int N, int K, void* c, int c_type,

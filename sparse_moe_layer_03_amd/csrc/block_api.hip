@@ -66,6 +66,11 @@ int check_product(const char* f, int N, int K, int kmul, int c_type) {
   return MOE_OK;
 }
 
+int check_out(const char* f, int P, int N) {
+  if ((int64_t)P * N > kMaxProductOut) return fail(MOE_ERR_SHAPE, "%s: %d rows of %d columns exceed 2^37", f, P, N);
+  return MOE_OK;
+}
+
 int quantize_args(const char* f, const uint16_t* x, int R, int K, int8_t* q, float* scale) {
   int rc = check_rows(f, R);
   if (rc) return rc;
@@ -82,7 +87,7 @@ int grouped(const char* f, const void* a, const float* a_scale, const void* b, c
             const int32_t* off, const int32_t* counts, const int32_t* rows, int a_div, int P, int R, int E, int N,
             int K, void* c, int c_type, bool i8, void* stream) {
   int rc = check_product(f, N, K, i8 ? 16 : 8, c_type);
-  if (rc || (rc = check_rows(f, P)) || (rc = check_rows(f, R))) return rc;
+  if (rc || (rc = check_rows(f, P)) || (rc = check_rows(f, R)) || (rc = check_out(f, P, N))) return rc;
   if (E < 1 || E > kMaxE) return fail(MOE_ERR_SHAPE, "%s: E=%d outside [1, %d]", f, E, kMaxE);
   if (a_div < 1) return fail(MOE_ERR_SHAPE, "%s: a_div=%d must be at least 1", f, a_div);
   if (P == 0 || R == 0) return ok();
@@ -155,7 +160,7 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const fl
                 const uint16_t* add, int M, int N, int K, void* c, int c_type, void* stream) {
   const char* f = "moe_gemm_i8";
   int rc = check_product(f, N, K, 16, c_type);
-  if (rc || (rc = check_rows(f, M))) return rc;
+  if (rc || (rc = check_rows(f, M)) || (rc = check_out(f, M, N))) return rc;
   if (M == 0) return ok();
   if (!a || !a_scale || !b || !b_scale || !c)
     return fail(MOE_ERR_NULL, "%s: a, a_scale, b, b_scale and c are required", f);

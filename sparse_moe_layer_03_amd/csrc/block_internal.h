@@ -11,6 +11,7 @@ constexpr int kMaxQuantK = 32768;  // likewise a quantised row
 constexpr int kMaxProductK = 65536;  // 2^14 * K stays below 2^31: the int32 sums of 8-bit products cannot overflow
 constexpr int kMaxProductN = 1 << 20;
 constexpr int kMaxProductRows = 1 << 28;
+constexpr int64_t kMaxProductOut = (int64_t)1 << 37;  // positions times columns: output elements of 256 GB in bf16
 
 // Rows are quantised against at least this magnitude, so that the scale and its inverse stay normal floats.
 constexpr float kQuantTiny = 0x1p-100f;

@@ -282,6 +282,8 @@ __device__ __forceinline__ int swz_term(int row) { return ((row >> 1) ^ ((row & 
 // few distinct rows and columns at a time.
 constexpr int kGroupM = 4;
 
+constexpr int kMaxItems = 1 << 23;
+
 struct ProductItem {
   int expert, first, rows, n0;
   int only;  // the expert's only tile
@@ -309,9 +311,10 @@ struct ProductList {
       int first = 0, count = 0;
       if (e < p.E) expert_range(p, e, first, count);
       start[i] = sum;
-      // the bound, beyond any product that fits the memory, keeps 256 counts in an int whatever off and counts hold
+      // the launch keeps experts that share the positions below the bound; it keeps 256 counts in an int whatever
+      // off and counts hold
       const int64_t items = (int64_t)((count + BM - 1) / BM) * nbn;
-      sum += (int)(items < (1 << 23) ? items : (1 << 23) - 1);
+      sum += (int)(items < kMaxItems ? items : kMaxItems - 1);
     }
     int incl = sum;
 #pragma unroll
@@ -637,15 +640,17 @@ hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
   } tiles[] = {
       {256, 256, 1.8f}, {128, 256, 1.1f}, {64, 128, 0.43f}, {32, 128, 0.36f}, {32, 64, p.Kb < 2048 ? 0.19f : 0.175f}};
   constexpr int kFirst = NT ? 1 : 0;  // below a mean of 64 rows the largest tile is never the best
-  int best = kFirst;
-  float least = 0.0f;
+  int best = 1;
+  float least = INFINITY;
   for (int i = kFirst; i < 5; ++i) {
-    const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1
-                               : ((int64_t)p.P + tiles[i].bm - 1) / tiles[i].bm;
-    const int64_t items = rows * ((p.N + tiles[i].bn - 1) / tiles[i].bn);
+    const int64_t cols = (p.N + tiles[i].bn - 1) / tiles[i].bn, all = ((int64_t)p.P + tiles[i].bm - 1) / tiles[i].bm;
+    // far more positions than rows: the item list counts to kMaxItems (with kMaxProductOut 128 x 256 tiles stay below)
+    if ((all + (p.E < p.P ? p.E : p.P)) * cols > kMaxItems) continue;
+    const int64_t rows = p.off ? p.R / tiles[i].bm + (p.E < p.R ? p.E : p.R) / 2 + 1 : all;
+    const int64_t items = rows * cols;
     const float rounds = items <= 512 ? (float)((items + 255) / 256) : (float)items / 256.0f;
     const float t = rounds * tiles[i].cost;
-    if (i == kFirst || t < least) best = i, least = t;
+    if (t < least) best = i, least = t;
   }
   switch (best) {
     case 0:

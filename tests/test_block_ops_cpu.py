@@ -96,6 +96,14 @@ def test_grouped_refusals(L, kw, status):
     assert call(lambda *a: L.moe_grouped_gemm_i8(P, P, P, P, *a), GROUP, GROUP_ORDER, **kw) == want
 
 
+def test_outputs_beyond_the_item_list(L):
+    """Positions times columns above 2^37, whether or not the output rows are as many."""
+    assert call(L.moe_gemm_i8, GEMM, GEMM_ORDER, M=1 << 28, N=520) == moe.MOE_ERR_SHAPE
+    for kw in (dict(P=1 << 28, N=520), dict(P=(1 << 17) + 1, N=1 << 20)):
+        assert call(lambda *a: L.moe_grouped_gemm(P, P, *a), GROUP, GROUP_ORDER, **kw) == moe.MOE_ERR_SHAPE
+        assert call(lambda *a: L.moe_grouped_gemm_i8(P, P, P, P, *a), GROUP, GROUP_ORDER, **kw) == moe.MOE_ERR_SHAPE
+
+
 def test_grouped_missing_operands(L):
     tail = [GROUP[n] for n in GROUP_ORDER]
     assert L.moe_grouped_gemm(None, P, *tail) == moe.MOE_ERR_NULL

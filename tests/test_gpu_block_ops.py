@@ -372,6 +372,22 @@ def test_grouped_offsets_out_of_range_are_clipped(torch):
         assert bool(((c == 0) | (c == K)).all()) and bool((c[P:] == 0).all())
 
 
+def test_many_more_positions_than_rows(torch):
+    """A million positions for four rows of 16384 columns, the named ones first, inside and last: the tile goes by the
+    rows, the item list by the positions (2^23 items of the smallest tile)."""
+    P, R, N, K = (1 << 20) + 7, 4, 1 << 14, 16
+    g = B.gen(77)
+    a, b = B.ints(g, (R, K), -8, 8, torch.bfloat16), B.ints(g, (2, N, K), -8, 8, torch.bfloat16)
+    rows = torch.full((P,), -1, dtype=torch.int32, device="cuda")
+    for pos, i in ((0, 2), (5, 0), (600_000, 3), (P - 1, 1)):
+        rows[pos] = i
+    off = torch.tensor([0, 5, P], dtype=torch.int32, device="cuda")
+    c = torch.full((R, N), -777.0, device="cuda")
+    moe.moe_grouped_gemm(a, b, off, None, rows, 1, P, R, 2, N, K, c)
+    ref = torch.stack([a[i].double() @ b[0 if i == 2 else 1].double().t() for i in range(R)]).float()
+    same_bits(torch, c, ref, "c")
+
+
 @pytest.mark.parametrize("rows_of_a", [140_000, 270_000])
 def test_large_a_offsets(torch, rows_of_a):
     """A rows beyond 2^31 and beyond 2^32 bytes, gathered and in order."""
