@@ -112,6 +112,8 @@ class DeviceLayer:
             if s.I_s:
                 self.q["s_gu"], self.q["s_gu_scale"] = stacked(W["ws_gate"], W["ws_up"], 1, s.I_s, s.H)
                 self.q["s_down"], self.q["s_down_scale"] = rows(W["ws_down"], s.H, s.I_s)
+            # the first forward may run on any stream
+            torch.cuda.current_stream().synchronize()
 
     def workspace(self, T: int):
         s = self.shapes

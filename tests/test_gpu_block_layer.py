@@ -179,6 +179,23 @@ def test_side_stream(torch):
         del junk
 
 
+def test_weights_are_ready_for_any_stream(torch):
+    """The constructor's quantisation has ended when it returns, also behind other work of its stream."""
+    wl = synth.Workload("block", T=8, I_s=128, **SMALL)
+    inp = synth.make_inputs(wl, seed=4)
+    junk = torch.randn(4096, 4096, device="cuda")
+    for _ in range(20):
+        junk = junk @ junk * 1e-3
+    lay = DeviceLayer.from_inputs(inp, i8=True)
+    assert torch.cuda.current_stream().query()
+    st = torch.cuda.Stream()
+    x = G.to_dev_x(inp).contiguous()
+    torch.cuda.synchronize()
+    y = lay.forward(x, torch.zeros_like(x), stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(y, lay.forward(x))
+
+
 def test_graph_replays(torch):
     """A captured block replayed with new inputs, eager work between the replays; two graphs of two layers in turn."""
     inp, lay, _ = layer(128)
