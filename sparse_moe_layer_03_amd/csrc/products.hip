@@ -249,10 +249,12 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
 // 16 (4) bytes per lane from src to LDS at lds_base + 16 (4) * lane; lds_base is wave-uniform.  Inline assembly, so
 // that the compiler's wait counts do not order LDS reads behind loads in flight; the K loop waits itself.
 __device__ __forceinline__ void to_lds16(const void* src, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(src)
+               : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds4(const void* src, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(src)
+               : "memory", "m0");
 }
 // The K loop's form: a wave-uniform base and 32-bit lane offsets that stay the same from step to step, so that a load
 // costs no vector instruction (dense 8-bit 8192 x 4096 x 4096 132 -> 124 us, grouped bf16 prefill 394 -> 376 us).
@@ -261,10 +263,10 @@ template <bool NT>
 __device__ __forceinline__ void to_lds16(const char* base, uint32_t off, uint32_t lds_base) {
   if constexpr (NT)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds_base), "v"(off), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
