@@ -38,12 +38,17 @@ __device__ __forceinline__ i32x16 mma32(const u32x4& b, const u32x4& a, const i3
 
 __device__ const u32x4 kZeros[1] = {{0u, 0u, 0u, 0u}};  // source of the chunks behind a row's end
 
-// Positions of expert e, kept inside [0, P).
+// The positions of a run that begins at off, cut to [0, P): n of them, or up to n where it is the run's end.  No step
+// leaves an int, whatever the three values hold.
+__device__ __forceinline__ void cut_run(int P, int off, int n, bool is_end, int& first, int& count) {
+  first = min(max(off, 0), P);
+  const int len = is_end ? max(n, first) - first : max(n, 0) + min(off, 0);
+  count = min(max(len, 0), P - first);
+}
+
+// Positions of expert e.
 __device__ __forceinline__ void expert_range(const ProductArgs& p, int e, int& first, int& count) {
-  const int lo = min(max(p.off[e], 0), p.P);
-  const int n = p.counts ? p.counts[e] : p.off[e + 1] - lo;
-  first = lo;
-  count = min(max(n, 0), p.P - lo);
+  cut_run(p.P, p.off[e], p.counts ? p.counts[e] : p.off[e + 1], !p.counts, first, count);
 }
 
 // The same for an expert that is the same in all lanes, by scalar loads: a vector load would wait behind the ring's.
@@ -51,10 +56,7 @@ __device__ __forceinline__ void expert_range(const ProductArgs& p, int e, int& f
 __device__ __forceinline__ void expert_range_scalar(const ProductArgs& p, int e, int& first, int& count) {
   typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
   const scalar_ptr off = (scalar_ptr)(uintptr_t)p.off, counts = (scalar_ptr)(uintptr_t)p.counts;
-  const int lo = min(max(off[e], 0), p.P);
-  const int n = p.counts ? counts[e] : off[e + 1] - lo;
-  first = lo;
-  count = min(max(n, 0), p.P - lo);
+  cut_run(p.P, off[e], p.counts ? counts[e] : off[e + 1], !p.counts, first, count);
 }
 
 // Output row of a position, -1 for padding.
