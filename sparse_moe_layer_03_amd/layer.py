@@ -5,6 +5,7 @@ runs in the HIP kernels behind ``moe.py``.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -49,6 +50,10 @@ class DeviceLayer:
     ``i8``: the expert weights are quantised on the GPU to 8-bit integers with
     a scale per output row, and ``forward`` runs the experts in 8-bit integers
     with a scale per token, by the grouped products (see ``_forward_i8``).
+
+    Calls of one layer share its workspace: one on another stream than the
+    last has to be ordered behind it.  What a call allocates belongs to the
+    pool of the stream it is given (the current one by default).
     """
 
     def __init__(self, weights: Dict[str, np.ndarray], k: int, device="cuda:0", fp8: bool = False,
@@ -135,6 +140,25 @@ class DeviceLayer:
             self._ws_streams = []
         return self._ws, self._ws_bytes
 
+    def _pool(self, stream):
+        """The context in which memory for work on ``stream`` (None, a torch stream or a raw handle) is allocated: a
+        block of the current stream's pool may still be in use by work pending there."""
+        import torch
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int)
+                                 else stream)
+
+    def _output(self, T: int, stream):
+        """[T, H] for the kernels on ``stream`` to write; once dropped, reused only behind the current stream's work at
+        that time, which may read it."""
+        import torch
+        with self._pool(stream):
+            y = torch.empty((T, self.shapes.H), dtype=torch.bfloat16, device=self.device)
+        if stream is not None:
+            y.record_stream(torch.cuda.current_stream(self.device))
+        return y
+
     def _note_stream(self, stream):
         """Remember a stream (None, a torch stream or a raw handle) the workspace is used on."""
         import torch
@@ -149,14 +173,14 @@ class DeviceLayer:
 
     def forward(self, x, y=None, stream=None):
         """y = layer(x); x is a [T, H] bfloat16 device tensor."""
-        import torch
         s = self.shapes
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
+            y = self._output(T, stream)
         if self.i8:
             return self._forward_i8(x, y, stream)
-        ws, nbytes = self.workspace(T)
+        with self._pool(stream):
+            ws, nbytes = self.workspace(T)
         self._note_stream(stream)
         W = self.w
         if self.q4:
@@ -228,7 +252,8 @@ class DeviceLayer:
         T = x.shape[0]
         if T == 0:
             return y
-        b = self._i8_buffers(T)
+        with self._pool(stream):
+            b = self._i8_buffers(T)
         self._note_stream(stream)
         n, E = T * s.k, s.E
         moe.moe_route(x, self.w["w_router"], self.bias, self.w["w_sg"], T, s.H, E, s.k, b["ids"], b["w"],
@@ -259,19 +284,16 @@ class DeviceLayer:
         import torch
         s = self.shapes
         T = r.shape[0]
-        # x belongs to the pool of the stream that uses it
-        st = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
-        with torch.cuda.stream(st):
+        if out is None:
+            out = self._output(T, stream)
+        with self._pool(stream):
             x = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
-        b = self._i8_buffers(T) if self.i8 and T > 0 else {"xq": None, "xs": None}
+            b = self._i8_buffers(T) if self.i8 and T > 0 else {"xq": None, "xs": None}
         moe.moe_block_norm(r, y, w_post, gate, w_pre, T, s.H, r, x, b["xq"], b["xs"], r_scale, y_scale, w_add, eps,
                            stream)
         if not self.i8:
-            out = self.forward(x, out, stream)
-        else:
-            out = torch.empty_like(x) if out is None else out
-            self._forward_i8(x, out, stream, quantized=True)
-        return out
+            return self.forward(x, out, stream)
+        return self._forward_i8(x, out, stream, quantized=True)
 
     # ---------------------------------------------------------------- stages
     def alloc_stage_buffers(self, T: int):
@@ -389,10 +411,9 @@ class PrefillRunner:
 
     def run(self, x, y=None, stream=None):
         """y = layer(x) for a [T, H] bfloat16 device tensor, segment by segment."""
-        import torch
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.layer.shapes.H), dtype=torch.bfloat16, device=self.layer.device)
+            y = self.layer._output(T, stream)
         moe.moe_prefill_runner_run(self.handle, x, T, y, stream)
         return y
 
