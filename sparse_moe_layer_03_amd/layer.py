@@ -171,14 +171,36 @@ class DeviceLayer:
         if all(st != u for u in self._ws_streams):
             self._ws_streams.append(st)
 
+    def _check_tensors(self, *tensors):
+        """Refuses, before anything is enqueued, tensors given as (name, tensor, shapes, dtypes) that the kernels would
+        misread or write astray: another shape, type, order or device than the layer's, which is the current one."""
+        at = self.w["w_router"].get_device()
+        for name, t, shapes, dtypes in tensors:
+            if t.dtype in dtypes and t.shape in shapes and t.is_contiguous() and t.get_device() == at >= 0:
+                continue
+            if t.dtype not in dtypes:
+                raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(map(str, dtypes))}")
+            if t.shape not in shapes:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            raise ValueError(f"{name} is on {t.device}, the layer on {self.w['w_router'].device}")
+        if at != moe._device():
+            raise ValueError(f"the layer is on GPU {at}; the current one is {moe._device()}")
+
     def forward(self, x, y=None, stream=None):
         """y = layer(x); x is a [T, H] bfloat16 device tensor."""
+        import torch
         s = self.shapes
         T = x.shape[0]
+        if self.i8:
+            rows, bf = ((T, s.H),), (torch.bfloat16,)
+            self._check_tensors(("x", x, rows, bf), *([] if y is None else [("y", y, rows, bf)]))
+            if y is None:
+                y = self._output(T, stream)
+            return self._forward_i8(x, y, stream)
         if y is None:
             y = self._output(T, stream)
-        if self.i8:
-            return self._forward_i8(x, y, stream)
         with self._pool(stream):
             ws, nbytes = self.workspace(T)
         self._note_stream(stream)
@@ -280,14 +302,20 @@ class DeviceLayer:
                       w_add: float = 0.0, eps: float = 1e-6, out=None, stream=None):
         """The layer as a block of a residual stream: r (in place) takes the previous block's output y (None: it has
         none) through moe_block_norm, and the layer runs on the normalised rows.  Returns the layer's output, which
-        the next block's moe_block_norm adds to r.  8-bit layers take the norm's quantised rows as they are."""
+        the next block's moe_block_norm adds to r.  8-bit layers take the norm's quantised rows as they are.
+        r is [T, H] bf16 or fp32; y and out are [T, H], w_pre and w_post [H], gate [H] or [T, H], all bf16."""
         import torch
         s = self.shapes
+        bf = torch.bfloat16
         T = r.shape[0]
+        rows, one = ((T, s.H),), ((s.H,), (1, s.H))
+        given = (("r", r, rows, (bf, torch.float32)), ("y", y, rows, (bf,)), ("w_pre", w_pre, one, (bf,)),
+                 ("w_post", w_post, one, (bf,)), ("gate", gate, one + rows, (bf,)), ("out", out, rows, (bf,)))
+        self._check_tensors(*(g for g in given if g[1] is not None))
         if out is None:
             out = self._output(T, stream)
         with self._pool(stream):
-            x = torch.empty((T, s.H), dtype=torch.bfloat16, device=self.device)
+            x = torch.empty((T, s.H), dtype=bf, device=self.device)
             b = self._i8_buffers(T) if self.i8 and T > 0 else {"xq": None, "xs": None}
         moe.moe_block_norm(r, y, w_post, gate, w_pre, T, s.H, r, x, b["xq"], b["xs"], r_scale, y_scale, w_add, eps,
                            stream)

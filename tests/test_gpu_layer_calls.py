@@ -1,7 +1,7 @@
-"""How a DeviceLayer is called: on other streams with the memory it allocates itself."""
+"""How a DeviceLayer is called: on other streams with the memory it allocates itself, and on the wrong device."""
 import pytest
 
-from sparse_moe_layer_03_amd import synth
+from sparse_moe_layer_03_amd import moe, synth
 from sparse_moe_layer_03_amd.layer import DeviceLayer, PrefillRunner
 from tests import gpu_util as G
 
@@ -90,3 +90,25 @@ def test_output_read_on_the_current_stream(torch, inp):
             torch.empty_like(want).fill_(float("nan"))
         torch.cuda.synchronize()
         assert torch.equal(z, want)
+
+
+@pytest.mark.parametrize("form", ["bf16", "i8"])
+def test_another_device_is_refused(torch, inp, form, monkeypatch):
+    """With another GPU as the current one, or tensors elsewhere, a call ends before the library is reached."""
+    lay, x = DeviceLayer.from_inputs(inp, **FORMS[form]), G.to_dev_x(inp)[:4]
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+
+    def no_library():
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(moe, "lib", no_library)
+    with pytest.raises(ValueError, match="y is on cpu, the layer on cuda:0"):
+        lay.forward_block(x, x.cpu(), w)
+    if form == "i8":
+        with pytest.raises(ValueError, match="x is on cpu, the layer on cuda:0"):
+            lay.forward(x.cpu())
+    monkeypatch.setattr(moe, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="the layer is on GPU 0; the current one is 1"):
+        lay.forward_block(x, None, w)
+    if form == "i8":
+        with pytest.raises(ValueError, match="the layer is on GPU 0; the current one is 1"):
+            lay.forward(x)
