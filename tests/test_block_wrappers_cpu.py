@@ -1,0 +1,64 @@
+"""The Python entry points of the operators around the layer refuse tensors that their sizes do not describe."""
+import pytest
+import torch
+
+from sparse_moe_layer_03_amd import moe
+
+BF, I8, F32, I32 = torch.bfloat16, torch.int8, torch.float32, torch.int32
+T, H, N, E = 4, 64, 32, 2
+
+
+class Reached(Exception):
+    """A call has passed its checks and asks for the library."""
+
+
+@pytest.fixture(autouse=True)
+def no_gpu_needed(monkeypatch):
+    def lib():
+        raise Reached
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    monkeypatch.setattr(moe, "lib", lib)
+
+
+def z(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+PRODUCT = dict(a_div=1, P=T, R=T, E=E, N=N, K=H, c=z(T, N), off=z(E + 1, dtype=I32), counts=None, rows=None)
+CALLS = {
+    "moe_block_norm": dict(r=z(T, H), y=z(T, H), w_post=z(H), gate=z(T, H), w_pre=z(H), T=T, H=H, r_out=z(T, H),
+                           x=z(T, H), q=z(T, H, dtype=I8), q_scale=z(T, dtype=F32)),
+    "moe_quantize_i8": dict(x=z(T, H), R=T, K=H, q=z(T, H, dtype=I8), scale=z(T, dtype=F32)),
+    "moe_swiglu_i8": dict(gu=z(T, 2 * H), row_gate=z(T, dtype=F32), R=T, I=H, q=z(T, H, dtype=I8),
+                          scale=z(T, dtype=F32)),
+    "moe_gemm_i8": dict(a=z(T, H, dtype=I8), a_scale=z(T, dtype=F32), b=z(N, H, dtype=I8), b_scale=z(N, dtype=F32),
+                        bias=None, add=z(T, N), M=T, N=N, K=H, c=z(T, N)),
+    "moe_grouped_gemm": dict(PRODUCT, a=z(T, H), b=z(E, N, H)),
+    "moe_grouped_gemm_i8": dict(PRODUCT, a=z(T, H, dtype=I8), a_scale=z(T, dtype=F32), b=z(E, N, H, dtype=I8),
+                                b_scale=z(E, N, dtype=F32)),
+}
+MATRICES = {"moe_block_norm": ("r", "y", "gate", "r_out", "x", "q"), "moe_quantize_i8": ("x", "q"),
+            "moe_swiglu_i8": ("gu", "q"), "moe_gemm_i8": ("a", "b", "add", "c"), "moe_grouped_gemm": ("a", "b", "c"),
+            "moe_grouped_gemm_i8": ("a", "b", "c")}
+
+
+@pytest.mark.parametrize("fn,name", [(f, m) for f, ms in MATRICES.items() for m in ms])
+def test_rows_of_another_length(fn, name):
+    args, t = CALLS[fn], CALLS[fn][name]
+    for bad in (torch.cat([t, t], dim=-1), t.reshape(-1, t.shape[-1] // 2)):
+        with pytest.raises(ValueError, match=f"^{name} has rows of {bad.shape[-1]} elements; expected {t.shape[-1]}$"):
+            getattr(moe, fn)(**{**args, name: bad})
+    # flat, of more dimensions, with more rows: the sizes describe these
+    for good in (t, t.reshape(-1), t.reshape(2, -1, t.shape[-1]), torch.cat([t, t], dim=0)):
+        with pytest.raises(Reached):
+            getattr(moe, fn)(**{**args, name: good})
+
+
+@pytest.mark.parametrize("name", ["w_post", "w_pre"])
+def test_norm_weights_are_one_row(name):
+    for bad in (z(2 * H), z(2, H), z(H, 2)):
+        with pytest.raises(ValueError, match=f"^{name} "):
+            moe.moe_block_norm(**{**CALLS["moe_block_norm"], name: bad})
+    with pytest.raises(Reached):
+        moe.moe_block_norm(**{**CALLS["moe_block_norm"], name: z(1, H)})
