@@ -321,9 +321,9 @@ ONE_ROW = -1
 
 def _args(*tensors):
     """Device pointers of tensors, given as (name, tensor, dtype, elements, row length) (None stays NULL, raw pointers
-    pass).  Refuses what the C ABI cannot tell from the right tensor: another type, too few elements, rows of another
-    length (a flat buffer has none; 0: any; ONE_ROW: more elements neither), strides, or another device than the current
-    one (whose stream the call is enqueued on)."""
+    pass, except for r, c and gate, whose type or size the calls read).  Refuses what the C ABI cannot tell from the
+    right tensor: another type, too few elements, rows of another length (a flat buffer has none; 0: any; ONE_ROW: more
+    elements neither), strides, or another device than the current one (whose stream the call is enqueued on)."""
     out = []
     dev = None
     for name, t, dtype, numel, row in tensors:
@@ -357,12 +357,15 @@ def _fault(name, t, dtype, numel, row) -> str:
 
 
 def _type(name, t):
-    """(MOE_BF16 or MOE_F32, the torch type) of a residual stream or a product's output."""
+    """(MOE_BF16 or MOE_F32, the torch type) of a residual stream or a product's output (None: the library's to
+    report)."""
     import torch
-    if t.dtype is torch.bfloat16:
-        return BF16, t.dtype
+    if t.__class__ is int:
+        raise ValueError(f"{name} must be a tensor: its type is the call's")
+    if t is None or t.dtype is torch.bfloat16:
+        return BF16, torch.bfloat16
     if t.dtype is torch.float32:
-        return F32, t.dtype
+        return F32, torch.float32
     raise ValueError(f"{name} is {t.dtype}; expected torch.bfloat16 or torch.float32")
 
 
@@ -372,6 +375,8 @@ def moe_block_norm(r, y, w_post, gate, w_pre, T, H, r_out, x, q, q_scale, r_scal
     import torch
     bf, n = torch.bfloat16, T * H
     r_type, rt = _type("r", r)
+    if gate.__class__ is int:
+        raise ValueError("gate must be a tensor: its size tells one row from T")
     gate_rows = 1 if gate is None or gate.numel() == H else T
     r, y, w_post, gate, w_pre, r_out, x, q, q_scale = _args(
         ("r", r, rt, n, H), ("y", y, bf, n, H), ("w_post", w_post, bf, H, ONE_ROW),

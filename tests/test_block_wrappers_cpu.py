@@ -62,3 +62,21 @@ def test_norm_weights_are_one_row(name):
             moe.moe_block_norm(**{**CALLS["moe_block_norm"], name: bad})
     with pytest.raises(Reached):
         moe.moe_block_norm(**{**CALLS["moe_block_norm"], name: z(1, H)})
+
+
+@pytest.mark.parametrize("fn", list(CALLS))
+def test_raw_pointers(fn):
+    """Raw pointers stand for every tensor but those whose type or size the call reads from them."""
+    raw = {k: 4096 if torch.is_tensor(v) and k not in ("r", "c", "gate") else v for k, v in CALLS[fn].items()}
+    with pytest.raises(Reached):
+        getattr(moe, fn)(**raw)
+    for name in {"r", "c", "gate"} & set(raw):
+        with pytest.raises(ValueError, match=f"^{name} must be a tensor"):
+            getattr(moe, fn)(**{**raw, name: 4096})
+
+
+@pytest.mark.parametrize("fn,name", [("moe_block_norm", "r"), ("moe_gemm_i8", "c"), ("moe_grouped_gemm", "c"),
+                                     ("moe_grouped_gemm_i8", "c")])
+def test_missing_tensors_are_the_librarys_to_report(fn, name):
+    with pytest.raises(Reached):
+        getattr(moe, fn)(**{**CALLS[fn], name: None})
