@@ -52,8 +52,10 @@ class DeviceLayer:
     with a scale per token, by the grouped products (see ``_forward_i8``).
 
     Calls of one layer share its workspace: one on another stream than the
-    last has to be ordered behind it.  What a call allocates belongs to the
-    pool of the stream it is given (the current one by default).
+    last has to be ordered behind it, and so have replays of captured calls.
+    A workspace that a captured call used is kept as long as the layer.  What
+    a call allocates belongs to the pool of the stream it is given (the
+    current one by default).
     """
 
     def __init__(self, weights: Dict[str, np.ndarray], k: int, device="cuda:0", fp8: bool = False,
@@ -87,7 +89,9 @@ class DeviceLayer:
         self.shapes = Shapes(H=H, E=E, k=k, I=I, I_s=I_s)
         self._ws = None
         self._ws_bytes = 0
-        self._ws_streams = []  # streams the current workspace has been used on since it was allocated
+        self._ws_streams = []  # handles of the streams the current workspace has been used on since it was allocated
+        self._ws_captured = False  # whether a captured call has used it
+        self._ws_kept = []  # earlier workspaces that graphs still write on replay
         self._i8_views = None  # (workspace address, T, the views forward uses) of 8-bit layers
         if i8:
             self._quantize_weights()
@@ -134,10 +138,13 @@ class DeviceLayer:
                 # the caching allocator tracks only the allocating stream: keep the old buffer from being
                 # handed out again before work already enqueued on the other streams that used it is done
                 for st in self._ws_streams:
-                    self._ws.record_stream(st)
+                    self._ws.record_stream(torch.cuda.ExternalStream(st, device=self.device))
+                if self._ws_captured:
+                    self._ws_kept.append(self._ws)
             self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
             self._ws_bytes = max(need, 256)
             self._ws_streams = []
+            self._ws_captured = False
         return self._ws, self._ws_bytes
 
     def _pool(self, stream):
@@ -160,16 +167,14 @@ class DeviceLayer:
         return y
 
     def _note_stream(self, stream):
-        """Remember a stream (None, a torch stream or a raw handle) the workspace is used on."""
+        """Remember what the workspace is used by: the stream (None, a torch stream or a raw handle), a capture."""
         import torch
-        if stream is None:
-            st = torch.cuda.current_stream(self.device)
-        elif isinstance(stream, int):
-            st = torch.cuda.ExternalStream(stream, device=self.device)
-        else:
-            st = stream
-        if all(st != u for u in self._ws_streams):
+        st = moe._stream(stream)
+        if st not in self._ws_streams:
             self._ws_streams.append(st)
+        if not self._ws_captured:
+            with self._pool(stream):
+                self._ws_captured = torch.cuda.is_current_stream_capturing()
 
     def _check_tensors(self, *tensors):
         """Refuses, before anything is enqueued, tensors given as (name, tensor, shapes, dtypes) that the kernels would

@@ -330,7 +330,7 @@ def _args(*tensors):
         if t is None or t.__class__ is int:
             out.append(t)
         elif (t.dtype is dtype and t.numel() >= numel and t.is_contiguous()
-              and (row == 0 or t.size(-1) == row or (t.dim() == 1 if row > 0 else t.numel() == numel))
+              and (row == 0 or t.shape[-1] == row or (t.dim() == 1 if row > 0 else t.numel() == numel))
               and (at := t.get_device()) >= 0):
             if at != dev:
                 dev = _device()

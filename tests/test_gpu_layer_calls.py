@@ -112,3 +112,36 @@ def test_another_device_is_refused(torch, inp, form, monkeypatch):
     if form == "i8":
         with pytest.raises(ValueError, match="the layer is on GPU 0; the current one is 1"):
             lay.forward(x)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+def test_captured_call_keeps_its_workspace(torch, inp, form):
+    """A larger batch after a capture gives the layer another workspace; the graph's own is not handed out to others,
+    and its replays stay right beside the program's other work."""
+    G.say(f"[captured] {form}")
+    lay, plain = (DeviceLayer.from_inputs(inp, **FORMS[form]) for _ in range(2))
+    x, T = G.to_dev_x(inp), 70
+    xs, y, st = x[:T].clone(), torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        lay.forward(xs, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        lay.forward(xs, y)
+    at, size = lay._ws.data_ptr(), lay._ws_bytes
+    big = lay.forward(x)
+    torch.cuda.synchronize()
+    assert lay._ws.data_ptr() != at
+    assert torch.equal(big, plain.forward(x))
+    held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    with torch.cuda.stream(st):
+        held += [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert not [h for h in held if at - size < h.data_ptr() < at + size]
+    for i in range(3):
+        xs.copy_(x[100 * i:100 * i + T])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, plain.forward(x[100 * i:100 * i + T])), f"replay {i}"
+        assert all(bool((h == 255).all()) for h in held)
