@@ -121,6 +121,9 @@ class DeviceLayer:
             if s.I_s:
                 self.q["s_gu"], self.q["s_gu_scale"] = stacked(W["ws_gate"], W["ws_up"], 1, s.I_s, s.H)
                 self.q["s_down"], self.q["s_down_scale"] = rows(W["ws_down"], s.H, s.I_s)
+            # as the grouped products take them
+            self._i8_experts = (self.q["gu"].view(s.E, 2 * s.I, s.H), self.q["gu_scale"].view(s.E, 2 * s.I),
+                                self.q["down"].view(s.E, s.H, s.I), self.q["down_scale"].view(s.E, s.H))
             # the first forward may run on any stream
             torch.cuda.current_stream().synchronize()
 
@@ -290,10 +293,11 @@ class DeviceLayer:
         if not quantized:
             moe.moe_quantize_i8(x, T, s.H, b["xq"], b["xs"], stream)
         P = b["sorted"].numel()
-        moe.moe_grouped_gemm_i8(b["xq"], b["xs"], q["gu"], q["gu_scale"], b["pad_off"], b["counts"], b["sorted"], s.k,
+        gu, gu_scale, down, down_scale = self._i8_experts
+        moe.moe_grouped_gemm_i8(b["xq"], b["xs"], gu, gu_scale, b["pad_off"], b["counts"], b["sorted"], s.k,
                                 P, n, E, 2 * s.I, s.H, b["gu"], stream)
         moe.moe_swiglu_i8(b["gu"], None, n, s.I, b["hq"], b["hs"], stream)
-        moe.moe_grouped_gemm_i8(b["hq"], b["hs"], q["down"], q["down_scale"], b["pad_off"], b["counts"], b["sorted"],
+        moe.moe_grouped_gemm_i8(b["hq"], b["hs"], down, down_scale, b["pad_off"], b["counts"], b["sorted"],
                                 1, P, n, E, s.H, s.I, b["o"], stream)
         moe.moe_combine(b["o"], b["w"], None, None, None, T, s.H, s.k, 0, y, stream)
         if s.I_s:

@@ -9,6 +9,7 @@ library has not been built, importing and calling fails loudly.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from typing import Optional
 
@@ -316,21 +317,17 @@ def moe_combine(o, w, h_s, ws_down, s, T, H, k, I_s, y, stream=None):
 
 
 # ------------------------------------------------------------- operators around the layer
-ONE_ROW = -1
-
-
 def _args(*tensors):
-    """Device pointers of tensors, given as (name, tensor, dtype, elements, row length) (None stays NULL, raw pointers
-    pass, except for r, c and gate, whose type or size the calls read).  Refuses what the C ABI cannot tell from the
-    right tensor: another type, too few elements, rows of another length (a flat buffer has none; 0: any; ONE_ROW: more
-    elements neither), strides, or another device than the current one (whose stream the call is enqueued on)."""
+    """Device pointers of tensors, given as (name, tensor, dtype, shape) (None stays NULL, raw pointers pass, except for
+    r, c and gate, whose type or size the calls read).  Refuses what the C ABI cannot tell from the right tensor:
+    another type, another shape (see _fits), strides, or another device than the current one (whose stream the call is
+    enqueued on)."""
     out = []
     dev = None
-    for name, t, dtype, numel, row in tensors:
+    for name, t, dtype, shape in tensors:
         if t is None or t.__class__ is int:
             out.append(t)
-        elif (t.dtype is dtype and t.numel() >= numel and t.is_contiguous()
-              and (row == 0 or t.shape[-1] == row or (t.dim() == 1 if row > 0 else t.numel() == numel))
+        elif (t.dtype is dtype and (t.shape == shape or _fits(name, t, shape)) and t.is_contiguous()
               and (at := t.get_device()) >= 0):
             if at != dev:
                 dev = _device()
@@ -338,21 +335,31 @@ def _args(*tensors):
                     raise ValueError(f"{name} is on GPU {at}; the current one is {dev}")
             out.append(t.data_ptr())
         else:
-            raise ValueError(_fault(name, t, dtype, numel, row))
+            raise ValueError(_fault(name, t, dtype, shape))
     return out
 
 
-def _fault(name, t, dtype, numel, row) -> str:
+def _fits(name, t, shape) -> bool:
+    """Whether a tensor of another shape holds one of this shape from its first element on: it is flat or its rows are
+    as long, and it has as many elements or more (the norms' weights: as many)."""
+    n = math.prod(shape)
+    if name in ("w_post", "w_pre"):
+        return t.numel() == n
+    return t.numel() >= n and (len(shape) == 1 or t.dim() < 2 or t.shape[-1] == shape[-1])
+
+
+def _fault(name, t, dtype, shape) -> str:
+    n = math.prod(shape)
     if t.dtype is not dtype:
         return f"{name} is {t.dtype}; expected {dtype}"
-    if t.numel() < numel:
-        return f"{name} has {t.numel()} elements; {numel} needed"
+    if t.numel() < n:
+        return f"{name} has {t.numel()} elements; {n} needed"
     if not t.is_contiguous():
         return f"{name} must be contiguous"
-    if row < 0 and t.numel() != numel:
-        return f"{name} has {t.numel()} elements; expected {numel}"
-    if row > 0 and t.dim() != 1 and t.size(-1) != row:
-        return f"{name} has rows of {t.size(-1)} elements; expected {row}"
+    if not _fits(name, t, shape):
+        if len(shape) == 1:
+            return f"{name} has {t.numel()} elements; expected {n}"
+        return f"{name} has rows of {t.shape[-1]} elements; expected {shape[-1]}"
     return f"{name} is on {t.device}, not on a GPU"
 
 
@@ -373,31 +380,31 @@ def moe_block_norm(r, y, w_post, gate, w_pre, T, H, r_out, x, q, q_scale, r_scal
                    w_add: float = 0.0, eps: float = 1e-6, stream=None):
     """The type of r (bf16 or fp32) is that of r_out; gate has H elements (one row for all tokens) or T * H."""
     import torch
-    bf, n = torch.bfloat16, T * H
+    bf, rows = torch.bfloat16, (T, H)
     r_type, rt = _type("r", r)
     if gate.__class__ is int:
         raise ValueError("gate must be a tensor: its size tells one row from T")
-    gate_rows = 1 if gate is None or gate.numel() == H else T
+    one = gate is None or gate.numel() == H
     r, y, w_post, gate, w_pre, r_out, x, q, q_scale = _args(
-        ("r", r, rt, n, H), ("y", y, bf, n, H), ("w_post", w_post, bf, H, ONE_ROW),
-        ("gate", gate, bf, gate_rows * H, H), ("w_pre", w_pre, bf, H, ONE_ROW), ("r_out", r_out, rt, n, H),
-        ("x", x, bf, n, H), ("q", q, torch.int8, n, H), ("q_scale", q_scale, torch.float32, T, 0))
-    _check(lib().moe_block_norm(r, r_type, y, w_post, gate, gate_rows, r_scale, y_scale, w_pre, w_add, eps, T, H, r_out,
-                                x, q, q_scale, _stream(stream)))
+        ("r", r, rt, rows), ("y", y, bf, rows), ("w_post", w_post, bf, (H,)),
+        ("gate", gate, bf, (H,) if one else rows), ("w_pre", w_pre, bf, (H,)), ("r_out", r_out, rt, rows),
+        ("x", x, bf, rows), ("q", q, torch.int8, rows), ("q_scale", q_scale, torch.float32, (T,)))
+    _check(lib().moe_block_norm(r, r_type, y, w_post, gate, 1 if one else T, r_scale, y_scale, w_pre, w_add, eps, T, H,
+                                r_out, x, q, q_scale, _stream(stream)))
 
 
 def moe_quantize_i8(x, R, K, q, scale, stream=None):
     import torch
-    x, q, scale = _args(("x", x, torch.bfloat16, R * K, K), ("q", q, torch.int8, R * K, K),
-                        ("scale", scale, torch.float32, R, 0))
+    x, q, scale = _args(("x", x, torch.bfloat16, (R, K)), ("q", q, torch.int8, (R, K)),
+                        ("scale", scale, torch.float32, (R,)))
     _check(lib().moe_quantize_i8(x, R, K, q, scale, _stream(stream)))
 
 
 def moe_swiglu_i8(gu, row_gate, R, I, q, scale, stream=None):
     import torch
     gu, row_gate, q, scale = _args(
-        ("gu", gu, torch.bfloat16, 2 * R * I, 2 * I), ("row_gate", row_gate, torch.float32, R, 0),
-        ("q", q, torch.int8, R * I, I), ("scale", scale, torch.float32, R, 0))
+        ("gu", gu, torch.bfloat16, (R, 2 * I)), ("row_gate", row_gate, torch.float32, (R,)),
+        ("q", q, torch.int8, (R, I)), ("scale", scale, torch.float32, (R,)))
     _check(lib().moe_swiglu_i8(gu, row_gate, R, I, q, scale, _stream(stream)))
 
 
@@ -407,9 +414,9 @@ def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
     i8, f32 = torch.int8, torch.float32
     c_type, ct = _type("c", c)
     a, a_scale, b, b_scale, bias, add, c = _args(
-        ("a", a, i8, M * K, K), ("a_scale", a_scale, f32, M, 0), ("b", b, i8, N * K, K),
-        ("b_scale", b_scale, f32, N, 0), ("bias", bias, f32, N, 0), ("add", add, torch.bfloat16, M * N, N),
-        ("c", c, ct, M * N, N))
+        ("a", a, i8, (M, K)), ("a_scale", a_scale, f32, (M,)), ("b", b, i8, (N, K)),
+        ("b_scale", b_scale, f32, (N,)), ("bias", bias, f32, (N,)), ("add", add, torch.bfloat16, (M, N)),
+        ("c", c, ct, (M, N)))
     _check(lib().moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, c_type, _stream(stream)))
 
 
@@ -423,8 +430,8 @@ def moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, stream=No
     bf, i32 = torch.bfloat16, torch.int32
     c_type, ct = _type("c", c)
     a, b, off, counts, rows, c = _args(
-        ("a", a, bf, _a_rows(a_div, R) * K, K), ("b", b, bf, E * N * K, K), ("off", off, i32, E + 1, 0),
-        ("counts", counts, i32, E, 0), ("rows", rows, i32, P, 0), ("c", c, ct, R * N, N))
+        ("a", a, bf, (_a_rows(a_div, R), K)), ("b", b, bf, (E, N, K)), ("off", off, i32, (E + 1,)),
+        ("counts", counts, i32, (E,)), ("rows", rows, i32, (P,)), ("c", c, ct, (R, N)))
     _check(lib().moe_grouped_gemm(a, b, off, counts, rows, a_div, P, R, E, N, K, c, c_type, _stream(stream)))
 
 
@@ -435,8 +442,8 @@ def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, 
     c_type, ct = _type("c", c)
     n = _a_rows(a_div, R)
     a, a_scale, b, b_scale, off, counts, rows, c = _args(
-        ("a", a, i8, n * K, K), ("a_scale", a_scale, f32, n, 0), ("b", b, i8, E * N * K, K),
-        ("b_scale", b_scale, f32, E * N, 0), ("off", off, i32, E + 1, 0), ("counts", counts, i32, E, 0),
-        ("rows", rows, i32, P, 0), ("c", c, ct, R * N, N))
+        ("a", a, i8, (n, K)), ("a_scale", a_scale, f32, (n,)), ("b", b, i8, (E, N, K)),
+        ("b_scale", b_scale, f32, (E, N)), ("off", off, i32, (E + 1,)), ("counts", counts, i32, (E,)),
+        ("rows", rows, i32, (P,)), ("c", c, ct, (R, N)))
     _check(lib().moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, c_type,
                                      _stream(stream)))
