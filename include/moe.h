@@ -448,8 +448,9 @@ int moe_block_norm(const void* r, int r_type, const uint16_t* y, const uint16_t*
 /*
  * Rows as 8-bit integers with one scale per row (a token's activations, a weight matrix's output
  * channels):  scale[r] = max(max_k |x[r,k]|, 2^-100) / 127,  q[r,k] = x[r,k] / scale[r] rounded to nearest
- * even (computed as x * (127 / max) in fp32), so |q| <= 127.  A row that holds an infinity or a NaN gets
- * scale NaN and codes 0: products with it are NaN, other rows are not touched by it.
+ * (x * (127 / max) in fp32, so that a quotient halfway between two codes may go to either), |q| <= 127.
+ * A row that holds an infinity or a NaN gets scale NaN and codes 0: products with it are NaN, other rows
+ * are not touched by it.
  *   x [R,K] bf16, q [R,K] int8, scale [R] fp32.  K % 16 == 0, 16 <= K <= 32768; R <= 2^28.
  */
 int moe_quantize_i8(const uint16_t* x, int R, int K, int8_t* q, float* scale, void* stream);
@@ -480,7 +481,7 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const fl
  * Expert e owns positions off[e] .. off[e] + n_e - 1 with n_e = counts[e] (counts NULL: off[e+1] - off[e]);
  * rows NULL: id = p.  Ids outside [0, R) are padding.  Rows of c that no position names are left as they
  * were; an expert may own no position; no two positions name one row.  off, counts, rows are read on the
- * device, and positions outside [0, P) are not touched.
+ * device; an expert's run may begin before 0 or end behind P, and positions outside [0, P) are not touched.
  *   moe_align's outputs serve as they are: off = pad_off, counts, rows = sorted, P = moe_align_max_rows,
  *   R = T*k; a_div = k reads token rows (gate/up), a_div = 1 assignment rows (down).
  *   a [(R-1)/a_div + 1, K], b [E,N,K], c [R,N] bf16 or fp32 (c_type); off [E+1], counts [E], rows [P] int32.

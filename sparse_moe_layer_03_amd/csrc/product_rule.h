@@ -23,12 +23,12 @@ struct ProductSize {
 // for the small tiles, which read the same rows more often than a grouped launch's weight streams leave room for.  The
 // narrowest tile costs half of the next, a little less where long rows hide its item changes.  Grouped launches count
 // half a tile of padding per expert.  Measured, us, tiles of 256 x 256 / 128 x 256 / 64 x 128 / 32 x 128 / 32 x 64:
-//   dense 8-bit, K 2048: 300 x 1024 25 / 16 / 8.2 / 6.6 / 6.4, 512 x 4096 26 / 17 / 9.5 / 12.5 / 14, 2048 x 2048 27 /
-//   18 / 15.8 / 22 / 25, 4096 x 4096 39 / 43 / 51 / 78 / 87
-//   bf16, 256 experts, top-8, K 2048, N 1024: 1 token (weights from HBM) - / - / 19 / 16 / 12, 32 tokens 88 / 68 / 59 /
-//   57 / 56, 512 tokens 152 / 124 / 126 / 123 / 129, 1024 tokens 161 / 151 / 162 / 176 / 187, 2048 tokens 208 / 189 /
-//   212 / 243 / 269, 8192 tokens 368 / 366 / - / - / -
-//   8-bit, K 512, N 2048: 128 tokens 36 / 29 / 27 / 26 / 28, 777 tokens 56 / 46 / 44 / 51 / 57
+//   dense 8-bit, K 2048: 300 x 1024 25 / 16 / 8.2 / 6.7 / 6.5, 512 x 4096 26 / 17 / 10.1 / 13.4 / 14.6, 2048 x 2048
+//   27 / 19 / 15.7 / 24 / 26, 4096 x 4096 38 / 42 / 51 / 77 / 87
+//   bf16, 256 experts, top-8, K 2048, N 1024: 1 token (weights from HBM) - / - / 19 / 15.8 / 13.5, 32 tokens 93 / 67 /
+//   59 / 57 / 55, 512 tokens 155 / 124 / 124 / 134 / 139, 1024 tokens 165 / 153 / 161 / 178 / 189, 2048 tokens 207 /
+//   189 / 211 / 245 / 270, 8192 tokens 368 / 366 / - / - / -
+//   8-bit, K 512, N 2048: 128 tokens 38 / 29 / 27 / 26 / 28, 777 tokens 57 / 46 / 43 / 51 / 56
 // (128 x 128: 10% less where it makes 256 dense items, 15.0 for 2048 x 2048, and more elsewhere; not among them.)
 inline int product_tile(const ProductSize& p, bool nt) {
   const struct {
@@ -54,8 +54,9 @@ inline int product_tile(const ProductSize& p, bool nt) {
 
 // Below a mean of 64 rows per expert a launch mostly streams weights: where they would not stay in the 256 MB
 // Infinity Cache in any case, those of an expert's only tile pass the caches by, which then keep the rows of A and
-// C.  With / without, us, bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 54.6 / 59.2, 512 tokens 118 / 137; at
-// a mean of 64 190 / 180, at 256 363 / 367; 1 token, 33 MB of weights, 13.4 / 11.1 repeated, 13.3 / 13.8 from HBM
+// C.  With / without, us, bf16, 256 experts, top-8, K 2048, N 1024: 32 tokens 55 / 62, 512 tokens 124 / 138, 1024 tokens
+// 152 / 161; at a mean of 64 189 / 189, at 256 363 / 367; 1 token, 33 MB of weights, 13.2 / 11.0 repeated, 13.3 / 13.5
+// from HBM
 inline bool product_streams(const ProductSize& p) {
   return p.live() / p.E < 64 && (int64_t)p.touched() * p.N * p.Kb > (128 << 20);
 }

@@ -239,9 +239,10 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
 // What bounds it: dense 8-bit 8192 x 4096 x 4096 takes 122 us (2.25 POP/s; a library's product 131 us); with the matrix
 // instructions taken out of a copy 98 us, with the loads taken out 95 us, with loads and LDS reads out 74 us: the parts
 // overlap to within a quarter.  Grouped bf16 gate/up rows of 8192 tokens (256 experts, top-8, most of them small) take
-// 367 us, 345 without the matrix instructions: 1.6 to 1.9 GB pass the L2 caches at the 5.2 TB/s that all CUs together
-// draw from beyond them (a direct-to-LDS load from L2 alone reaches 127 GB/s per CU).  Below a mean of about 64 rows
-// per expert the weights' stream is all: 32 tokens 53 us, 5.9 TB/s.
+// 367 us, 345 without the matrix instructions: 1.44 GB are read past the L2 caches and 0.135 written, 4.3 TB/s where a
+// plain read of 4 GiB reaches 6.8 (a direct-to-LDS load from L2 alone 127 GB/s per CU); the two-stage ring waits for
+// all loads at every step, and half of the experts fill a tile to less than a sixth.  Below a mean of about 64 rows per
+// expert the weights' stream is all: 32 tokens, some 77 experts, 55 us, 5.9 TB/s (a plain read of as much 5.9).
 //
 // Measured and not taken, dense / grouped in us against 128 / 390: four waves of 128 x 128 (spills) 143 / 457; loads
 // spread between the matrix instructions 134 / 425; the last sub-step's instructions behind the barrier 131 / 404;
@@ -295,7 +296,9 @@ struct ProductItem {
 // The item list of a launch: experts in order, within an expert groups of kGroupM row tiles, within a group column
 // blocks, within a block the group's tiles.  Lane l of every wave keeps the starts of experts 4 l .. 4 l + 3
 // in registers; each is read from its lane before one is selected, since a selection among the array's elements
-// would put it into scratch memory, whose loads wait behind the ring's (down rows of a chunk 48.0 -> 43.6 us).
+// would put it into scratch memory, whose loads wait behind the ring's (down rows of a chunk 48.0 -> 43.6 us).  One form
+// uses scratch memory still: fp32 output with bias or addend on the largest tile spills 4 or 6 registers around its
+// epilogue (8192 x 4096 x 4096 with addend 181 us against 150 to bf16, without 136 against 122).
 template <int BM, int BN>
 struct ProductList {
   int nbn, total;
