@@ -5,10 +5,10 @@
 // long as its sums need it, and written once.  A row has as many waves as let a lane hold one 16-byte chunk of it (up
 // to 16 waves; rows of up to 512 elements go four to a workgroup): fewer, fuller waves took longer in every norm, the
 // weights' loads waiting behind the reductions (one token of 2048 3.8 -> 2.7 us, 8192 tokens 31.1 -> 26.7, 3000 rows of
-// 16384 139 -> 83).  Now, with a copy of 1 GiB at 4.8 TB/s: norm behind, gate, add, norm before, 8192 x 2048 26.7 us
-// (5.0 TB/s); fp32 stream with a gate per token, 1021 x 4096 11.4 (5.1); norm before alone with r', 8192 x 2048, to bf16 rows 25.1,
-// to 8-bit rows 24.0, to both 29.5 (all from inputs outside the Infinity Cache); quantise 8192 x 4096 20.5 (4.9); SwiGLU rows
-// 65536 x 512 30.8 (5.4).
+// 16384 139 -> 83).  Now, with a copy of 1 GiB at 4.8 to 5.3 TB/s: norm behind, gate, add, norm before, 8192 x 2048 25.9
+// us (5.2 TB/s); fp32 stream with a gate per token, 1021 x 4096 11.4 (5.1); norm before alone with r', 8192 x 2048, to
+// bf16 rows 25.1, to 8-bit rows 24.0, to both 29.5 (these from inputs outside the Infinity Cache); quantise 8192 x 4096
+// 20.5 (4.9); SwiGLU rows 65536 x 512 30.8 (5.4).
 //
 // Sums run over a lane's chunks in order, then over the lanes in a fixed tree and the waves in order, so results do not
 // depend on scheduling.
