@@ -476,6 +476,21 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const fl
                 const uint16_t* add, int M, int N, int K, void* c, int c_type, void* stream);
 
 /*
+ * Matrix product in bf16 with its epilogue:
+ *     c[m,n] = act(sum_k a[m,k] b[n,k] + bias[n]) + add[m,n]
+ * in fp32, rounded once.  act: MOE_ACT_NONE, MOE_ACT_SILU v / (1 + e^-v), MOE_ACT_GELU in its tanh form,
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.
+ *   a [M,K], b [N,K] bf16, bias [N] fp32 or NULL, add [M,N] bf16 or NULL (may be c itself when c is bf16), c [M,N]
+ *   bf16 or fp32 (c_type).
+ *   K % 8 == 0, 8 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^20; M <= 2^28; M * N <= 2^37.  M = 0 is a successful no-op.
+ */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1
+#define MOE_ACT_GELU 2
+int moe_gemm(const uint16_t* a, const uint16_t* b, const float* bias, int act, const uint16_t* add, int M, int N, int K,
+             void* c, int c_type, void* stream);
+
+/*
  * Products grouped by expert over ragged row counts:
  *     c[id,:] = a[id / a_div,:] . b[e]^T      for every position p of expert e, id = rows[p]
  * Expert e owns positions off[e] .. off[e] + n_e - 1 with n_e = counts[e] (counts NULL: off[e+1] - off[e]);
@@ -497,6 +512,104 @@ int moe_grouped_gemm(const uint16_t* a, const uint16_t* b, const int32_t* off, c
 int moe_grouped_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale,
                         const int32_t* off, const int32_t* counts, const int32_t* rows, int a_div, int P, int R,
                         int E, int N, int K, void* c, int c_type, void* stream);
+
+/*
+ * Operators around attention, for the other half of a block: rotary positions, a paged cache, attention of new tokens
+ * over it.  The conventions above hold; rows of q, k, v and of outputs may lie further apart than they are long (x_ld
+ * and the like, elements from one row to the next, multiples of 8), so that the parts of one product's rows are used in
+ * place.  moe_attention alone takes a workspace; calls that share one have to be ordered by the caller, replays of
+ * captured calls included.  Inference only.
+ *
+ * Types of a cache (MOE_BF16 or):
+ */
+#define MOE_I8 2   /* signed 8-bit integers, a scale per token and head, top code 127 */
+#define MOE_E4M3 3 /* OCP FP8 E4M3 codes, a scale per token and head, top code 448    */
+
+/*
+ * Frequencies of rotary positions, in turns per token, for pairs i = 0 .. rot/2 - 1; host memory, host arithmetic.
+ *   MOE_ROPE_PLAIN   base^(-2 i / rot) / (2 pi)
+ *   MOE_ROPE_LINEAR  the same over `factor`: positions interpolated
+ *   MOE_ROPE_NTK     base replaced by base * factor^(rot / (rot - 2))
+ *   MOE_ROPE_YARN    pairs that turn more than 32 times within `original` tokens as plain, those that turn less than
+ *                    once as linear, a linear ramp over the pairs between; mscale = 0.1 ln(factor) + 1
+ * *mscale is 1 otherwise.  base > 1; factor >= 1 where used; original >= 1 where used.
+ */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_NTK 2
+#define MOE_ROPE_YARN 3
+int moe_rope_frequencies(int rot, double base, int scaling, double factor, double original, double* freq,
+                         float* mscale);
+
+/*
+ * Rotary positions: every head of a row, normed if w_norm is given, has its first rot elements rotated in pairs,
+ *     v = w_norm ? x / sqrt(mean(x^2) + eps) * (w_norm + w_add) : x        (mean over the head)
+ *     a = 2 pi pos[t] freq[i]
+ *     (v1, v2) -> mscale * (v1 cos a - v2 sin a, v2 cos a + v1 sin a)
+ * MOE_ROPE_HALF pairs elements (i, i + rot/2), MOE_ROPE_INTERLEAVED (2 i, 2 i + 1).  The angle's fraction of a turn is
+ * taken in 64 bits, the rest is fp32, rounded once.
+ *   x [T, heads*D] bf16, rows x_ld apart; out likewise, out_ld; out may be x (with x_ld = out_ld), else they do not
+ *   overlap.  pos [T] int32 (any value), freq [rot/2] double, on the device, both unused with rot = 0.
+ *   D % 8 == 0, 8 <= D <= 256; rot even, 0 <= rot <= D; heads <= 1024; T <= 2^24.
+ */
+#define MOE_ROPE_HALF 0
+#define MOE_ROPE_INTERLEAVED 1
+int moe_rope(const uint16_t* x, int64_t x_ld, const uint16_t* w_norm, float w_add, float eps, const int32_t* pos,
+             const double* freq, float mscale, int T, int heads, int D, int rot, int pairs, uint16_t* out,
+             int64_t out_ld, void* stream);
+
+/*
+ * A step's rows on their way to attention, in one launch: q normed and rotated to q_out as by moe_rope (w_q its norm),
+ * k likewise (w_k) into the cache, v into the cache as it is.
+ *   q [T, Hq*D], q_out; k, v [T, Hkv*D] bf16, rows q_ld, q_out_ld, k_ld, v_ld apart.  Hq = 0: no q (q, q_out, w_q
+ *   NULL).  q_out may be q (with equal strides).
+ *   slots [T] int32: token t goes to slot slots[t], page slots[t] / P, place slots[t] % P; slots outside
+ *   [0, n_pages * P) are padding and are not written; no two tokens name one slot.
+ *   k_cache, v_cache [n_pages, Hkv, P, D] of `type`; k_scale, v_scale [n_pages, Hkv, P] fp32 for 8-bit types, else
+ *   NULL.  A token's head is stored rounded to bf16, or as codes:  scale = max(max |x|, 2^-100) / top,
+ *   code = x / scale rounded to nearest (by x * (top / max) in fp32).  A head with an infinity or a NaN gets scale NaN
+ *   and codes 0.
+ *   P a power of two, 16 <= P <= 1024; n_pages * P <= 2^30; Hq, Hkv <= 1024; the rest as moe_rope.
+ */
+int moe_cache_write(const uint16_t* q, int64_t q_ld, const uint16_t* w_q, uint16_t* q_out, int64_t q_out_ld,
+                    const uint16_t* k, int64_t k_ld, const uint16_t* w_k, const uint16_t* v, int64_t v_ld, float w_add,
+                    float eps, const int32_t* pos, const double* freq, float mscale, const int32_t* slots, int T,
+                    int Hq, int Hkv, int D, int rot, int pairs, int type, int n_pages, int P, void* k_cache,
+                    void* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * Tokens read back from the cache (to move or inspect them): k[r], v[r] = code * scale of slot slots[r].
+ *   slots [n] int32; rows of slots outside [0, n_pages * P) are left as they were.  k, v [n, Hkv, D] bf16 or fp32
+ *   (out_type).  n <= 2^24; the rest as moe_cache_write.
+ */
+int moe_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int type,
+                   int n_pages, int P, const int32_t* slots, int n, int Hkv, int D, void* k, void* v, int out_type,
+                   void* stream);
+
+/*
+ * Causal attention of the new tokens of S sequences over the paged cache, which holds their keys and values already
+ * (moe_cache_write comes first); chunks of any length, single tokens included, may stand in one call.
+ *   Sequence s owns rows q_start[s] .. q_start[s+1] - 1 of q and has kv_len[s] keys, the new tokens' own the last of
+ *   them: its row i is at position p = kv_len[s] - n + i (n rows) and sees keys j with 0 <= j <= p and, with window
+ *   > 0, j > p - window.  Key j lies in page pages[s * max_pages + j / P], place j % P.
+ *     out = softmax_j(scale * q . k_j) v        per query head; head h reads key head h / (Hq / Hkv)
+ *   q, out [T, Hq*D] bf16, rows q_ld, out_ld apart, not overlapping.  lse [T, Hq] fp32 or NULL: ln sum_j e^(score),
+ *   for joining results over different keys.  Rows that see no key: out 0, lse -infinity.  Rows outside all sequences
+ *   are left as they were.
+ *   Keys that no row sees are not read into any sum, whatever their slots hold: entries of pages that hold visible
+ *   keys must lie in [0, n_pages) (else the rows that see them are NaN), others may hold anything.  kv_len beyond
+ *   max_pages * P counts as that; q_start is cut to [0, T].  All three are read on the device.
+ *   An infinity or a NaN in a key or value reaches the rows that see it and no others.
+ *   Hq % Hkv == 0; D 64, 128 or 256; scale > 0; T <= 2^24; T * Hq <= 2^30; S * Hkv <= 2^22; max_pages * P <= 2^30.
+ *   workspace: moe_attention_workspace_size bytes (0: none needed) for these T, S, heads and max_keys = max_pages * P,
+ *   16-byte aligned; it need not be cleared.  Scores, sums and out are fp32 until out is rounded; the softmax weights
+ *   are rounded to bf16 for their product with v (with T * (Hq / Hkv) <= 32 * S to a sum of two bf16 terms).
+ */
+size_t moe_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, int64_t max_keys);
+int moe_attention(const uint16_t* q, int64_t q_ld, const void* k_cache, const void* v_cache, const float* k_scale,
+                  const float* v_scale, int type, const int32_t* pages, const int32_t* q_start, const int32_t* kv_len,
+                  int T, int S, int Hq, int Hkv, int D, int n_pages, int P, int max_pages, float scale, int window,
+                  uint16_t* out, int64_t out_ld, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

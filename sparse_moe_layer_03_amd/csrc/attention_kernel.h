@@ -1,0 +1,688 @@
+// Attention of new tokens over a paged cache: the kernels, instantiated per type of the cache by attention_*.hip.
+//
+// Rows are (token, query head) pairs of one key head: row r of a sequence is token r / G, head r % G of the key head's
+// G query heads, so that all of them read the key head's cache once.  Per 32 rows and 32 keys
+//   S^T = K Q^T      lane l holds query row l & 31, keys 8 g + 4 (l >> 5) + i in register 4 g + i
+//   O^T = V^T P^T    the same lanes hold the row's P, which the instruction takes as they are: its 16 keys a step are
+//                    numbered 4 h + i and 8 + 4 h + i of lane half h, and V^T is read from LDS in that order, transposed
+//                    by the LDS read itself
+// so neither S nor P leaves its lane.  Softmax is the online form in base 2: running maximum m, sum l and O in fp32,
+// rescaled when a tile raises m by more than 2^kSlack.  P is rounded to bf16 for its product, an error of the size of
+// the output's own rounding (half a step, 2^-8 of each weight); where few rows leave the matrix cores idle the rest of it
+// goes in as a second bf16 term (2^-16).  l sums the unrounded values.
+//
+// A masked key has P = 0, which does not undo an Inf or NaN in its V: rows behind the range of keys that the tile's
+// rows can see are zeroed on the way into LDS; a key inside it that only some rows see (later tokens, the window's
+// edge) could still poison the others, which shows as a non-finite O.  Rows with one are computed again, key by key
+// over the visible ones alone, at the end (`careful`).
+#pragma once
+
+#include <atomic>
+
+#include "attend_internal.h"
+
+namespace moe {
+namespace attn {
+
+constexpr float kSlack = 8.0f;
+constexpr float kNegInf = -__builtin_inff();
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// D: head elements; CT: type of the cache; WR waves of 32 rows share a tile of KT keys; WK waves take every WK-th tile.
+template <int D_, int CT_, int WR_, int WK_, int KT_>
+struct Cfg {
+  static constexpr int D = D_, CT = CT_, WR = WR_, WK = WK_, KT = KT_;
+  static constexpr bool QUANT = CT != MOE_BF16;
+  static constexpr int R = 32 * WR;            // rows of a workgroup
+  static constexpr int UNIT = KT * WK;         // keys of a unit of work
+  static constexpr int GT = 64 * WR;           // threads that load a tile
+  static constexpr int THREADS = GT * WK;
+  static constexpr int ROWB = D * (QUANT ? 1 : 2);
+  static constexpr int CPR = ROWB / 16;        // 16-byte chunks of a cached row
+  static constexpr int CHUNKS = KT * CPR;
+  static constexpr int NL = (CHUNKS + GT - 1) / GT;
+  static constexpr int NS = QUANT ? (2 * KT + GT - 1) / GT : 1;  // scales a thread loads
+  static constexpr int NB = WR == 1 ? 1 : 2;   // tiles in LDS: a wave alone needs no second one
+  static constexpr int TILE = KT * D * 2;      // bytes of a tile's K or V in LDS, bf16
+  static constexpr int SCALES = QUANT ? 2 * KT * 4 : 0;
+  static constexpr int STAGE = 2 * TILE + SCALES;
+  static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
+  static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
+  static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
+  static_assert(WK == 1 || WR == 1, "");
+  static_assert(WK == 1 || STAGE >= 32 * D * 4, "the waves' O are merged in their tiles");
+  static_assert(LDS <= 160 * 1024, "");
+};
+
+struct Seq {
+  int q0, n, len;  // first row of q, new tokens, keys
+};
+__device__ __forceinline__ Seq seq_at(const AttentionArgs& p, int s) {
+  Seq q;
+  q.q0 = min(max(p.q_start[s], 0), p.T);
+  q.n = max(min(max(p.q_start[s + 1], 0), p.T) - q.q0, 0);
+  q.len = min(max(p.kv_len[s], 0), p.max_pages << p.page_shift);
+  return q;
+}
+// First key that any of the sequence's rows sees, down to a multiple of 64: where its units begin.
+__device__ __forceinline__ int seq_base(const AttentionArgs& p, const Seq& q) {
+  return p.window > 0 ? max(q.len - q.n - p.window + 1, 0) & ~63 : 0;
+}
+template <class C>
+__device__ __forceinline__ int seq_units(const AttentionArgs& p, const Seq& q) {
+  return max((q.len - seq_base(p, q) + C::UNIT - 1) / C::UNIT, 1);
+}
+template <class C>
+__device__ __forceinline__ int row_tiles(const AttentionArgs& p, const Seq& q) {
+  return (int)(((int64_t)q.n * p.G + C::R - 1) / C::R);
+}
+// Units of work of a sequence: all its row tiles and key heads times its keys.
+template <class C>
+__device__ __forceinline__ int64_t seq_work(const AttentionArgs& p, int s) {
+  const Seq q = seq_at(p, s);
+  return (int64_t)p.Hkv * row_tiles<C>(p, q) * seq_units<C>(p, q);
+}
+
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+// Sum of weight(s) over all sequences.
+template <class W>
+__device__ __forceinline__ int64_t sum_all(int S, int lane, W weight) {
+  int64_t sum = 0;
+  for (int b = 0; b < S; b += 64) sum += b + lane < S ? weight(b + lane) : 0;
+  return __shfl(wave_scan(sum, lane), 63);
+}
+// The sequence in which the running sum of weights passes `at`, and the sum before it; S if none does.
+template <class W>
+__device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64_t& before) {
+  before = 0;
+  for (int b = 0; b < S; b += 64) {
+    const int64_t incl = before + wave_scan(b + lane < S ? weight(b + lane) : 0, lane);
+    const int n = __popcll(__ballot(incl <= at));
+    if (n < 64) {
+      if (n > 0) before = __shfl(incl, n - 1);
+      return b + n;
+    }
+    before = __shfl(incl, 63);
+  }
+  return S;
+}
+
+// Scores and sums are kept by lane halves; both halves' maximum or sum.
+__device__ __forceinline__ float halves_max(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(x[0]) + __uint_as_float(x[1]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 16-byte chunk c of row r of a tile in LDS.  K: a read takes one chunk of 16 and more consecutive rows.  V: a
+// transposing read takes four rows of two neighbouring chunks.
+template <int D>
+__device__ __forceinline__ int k_at(int r, int c) {
+  if constexpr (D == 64) return r * 8 + (c ^ (((r >> 1) ^ ((r & 1) << 2)) & 7));
+  return r * (D / 8) + (c ^ (r & 15));
+}
+template <int D>
+__device__ __forceinline__ int v_at(int r, int c) {
+  if constexpr (D == 64) return r * 8 + (c ^ (((r >> 1) & 1) << 2));
+  return r * (D / 8) + (c ^ ((r & 3) << 2));
+}
+
+// Sixteen codes as two chunks of bf16 (every code is one exactly).
+template <int CT>
+__device__ __forceinline__ void widen(const u32x4& w, u32x4& lo, u32x4& hi) {
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (CT == MOE_E4M3) {
+      o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false));
+      o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true));
+    } else {
+      const int v = (int)w[i];
+      o[2 * i] = cvt_bf16x2((float)(v << 24 >> 24), (float)(v << 16 >> 24));
+      o[2 * i + 1] = cvt_bf16x2((float)(v << 8 >> 24), (float)(v >> 24));
+    }
+  }
+  lo = u32x4{o[0], o[1], o[2], o[3]}, hi = u32x4{o[4], o[5], o[6], o[7]};
+}
+
+template <int CT>
+__device__ __forceinline__ float cached(const void* p, int64_t i) {
+  if constexpr (CT == MOE_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  if constexpr (CT == MOE_I8) return (float)static_cast<const int8_t*>(p)[i];
+  return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p)[i], 0);
+}
+
+// Partial results in the workspace: per slot R rows of O (unscaled, fp32), then R pairs (m, l).
+template <class C>
+__device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
+  return p.partial + (size_t)slot * C::R * (C::D + 2);
+}
+
+// One workgroup computes one (sequence, key head, row tile), or (STREAM) its equal share of all units of work, which
+// may begin and end inside such an item: what is not a whole item goes to the workspace, slot 2 w for the end of an item
+// and 2 w + 1 for a beginning, and combine_kernel joins it.
+template <class C, bool STREAM>
+__device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, unsigned char* smem) {
+  constexpr int D = C::D, KT = C::KT, WR = C::WR, WK = C::WK;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave % WR, wk = wave / WR, gt = tid % C::GT;
+  const int hh = lane >> 5, ql = lane & 31;
+
+  unsigned char* group = smem + wk * C::NB * C::STAGE;
+
+  // ---- this workgroup's work
+  int64_t u = 0, u_end = 1, before = 0;
+  int s, h = 0, m = 0;
+  if constexpr (STREAM) {
+    auto weight = [&](int i) { return seq_work<C>(p, i); };
+    const int64_t total = sum_all(p.S, lane, weight);
+    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
+    u = blockIdx.x * per, u_end = min(total, u + per);
+    if (u >= u_end) return;
+    s = find(p.S, lane, u, weight, before);
+  } else {
+    auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at(p, i)); };
+    // the last tiles, which see the most keys, first
+    const int64_t tiles = gridDim.x / p.Hkv;
+    h = blockIdx.x % p.Hkv;
+    s = find(p.S, lane, tiles - 1 - blockIdx.x / p.Hkv, weight, before);
+    if (s >= p.S) return;
+    m = (int)(tiles - 1 - blockIdx.x / p.Hkv - before);
+  }
+  s = __builtin_amdgcn_readfirstlane(s);
+
+  while (u < u_end) {
+    const Seq q = seq_at(p, s);
+    const int units = seq_units<C>(p, q), base = seq_base(p, q);
+    int unit_lo = 0, unit_hi = units;
+    if constexpr (STREAM) {
+      const int tiles = row_tiles<C>(p, q);
+      const int64_t work = (int64_t)p.Hkv * tiles * units;
+      if (u >= before + work) {
+        before += work;
+        ++s;
+        continue;
+      }
+      const int64_t at = u - before, item = at / units;
+      unit_lo = (int)(at - item * units);
+      unit_hi = (int)min((int64_t)units, unit_lo + (u_end - u));
+      h = (int)(item / tiles), m = (int)(item - (int64_t)h * tiles);
+    }
+    const bool whole = unit_lo == 0 && unit_hi == units;
+    // ---- rows
+    const int n_rows = q.n * p.G, r0 = m * C::R, wrow = r0 + wr * 32;
+    const int pos0 = q.len - q.n;  // of token 0
+    const int i_first = r0 / p.G, i_last = (min(r0 + C::R, n_rows) - 1) / p.G;
+    // keys that the tile's rows see
+    const int kb = p.window > 0 ? max(pos0 + i_first - p.window + 1, 0) : 0;
+    const int ke = min(q.len, pos0 + i_last + 1);
+    const bool wave_live = wrow < n_rows;
+    const int w_lo = pos0 + min(wrow, n_rows - 1) / p.G, w_hi = pos0 + (min(wrow + 32, n_rows) - 1) / p.G;
+    const int row = wrow + ql;
+    const bool live = row < n_rows;
+    const int tok = live ? row / p.G : 0, head = h * p.G + (live ? row - tok * p.G : 0);
+    const int pos = live ? pos0 + tok : -1;
+    const int vis0 = p.window > 0 ? max(pos - p.window + 1, 0) : 0, vis_n = max(pos - vis0 + 1, 0);
+
+    bf16x8 qf[C::NQ];
+    {
+      const uint16_t* qp = p.q + (q.q0 + tok) * p.q_ld + (int64_t)head * D + 8 * hh;
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (live) v = *reinterpret_cast<const u32x4*>(qp + 16 * i);
+        qf[i] = __builtin_bit_cast(bf16x8, v);
+      }
+    }
+    // ---- tiles: tile j of this wave's group begins at key_of(j)
+    const int u_first = ke > kb ? max(unit_lo, (kb - base) / C::UNIT) : 0;
+    const int u_last = ke > kb ? min(unit_hi, (ke - base + C::UNIT - 1) / C::UNIT) : 0;
+    const int nt = max(u_last - u_first, 0);
+    auto key_of = [&](int j) { return base + ((u_first + j) * WK + wk) * KT; };
+    const int32_t* pages = p.pages + (int64_t)s * p.max_pages;
+    const int page_mask = (1 << p.page_shift) - 1;
+
+    u32x4 rk[C::NL], rv[C::NL];
+    float rs[C::NS];
+    unsigned bad = 0;  // bit i: load i's page is none
+    auto page_of = [&](int key) { return pages[min(max(key, kb), ke - 1) >> p.page_shift]; };
+    // the 64 lanes of a load read rows of one page: they begin at a multiple of, and are at most, 16
+    auto issue = [&](int j) {
+      const int k0 = key_of(j);
+      bad = 0;
+#pragma unroll
+      for (int i = 0; i < C::NL; ++i) {
+        const int c0 = i * C::GT + wr * 64;
+        if (C::CHUNKS % C::GT != 0 && c0 >= C::CHUNKS) break;
+        const int key = k0 + c0 / C::CPR;
+        int page = page_of(key);
+        if ((unsigned)page >= (unsigned)p.n_pages) page = 0, bad |= 1u << i;
+        const int64_t at = ((((int64_t)page * p.Hkv + h) << p.page_shift) + (key & page_mask)) * C::ROWB + lane * 16;
+        rk[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k_cache) + at);
+        rv[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.v_cache) + at);
+      }
+      if constexpr (C::QUANT) {
+#pragma unroll
+        for (int i = 0; i < C::NS; ++i) {
+          const int x = i * C::GT + gt, key = k0 + x % KT;
+          rs[i] = 0.0f;
+          if (x < 2 * KT && key >= kb && key < ke) {
+            const int page = page_of(key);
+            if ((unsigned)page < (unsigned)p.n_pages)
+              rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)page * p.Hkv + h) << p.page_shift) +
+                                                       (key & page_mask)];
+          }
+        }
+      }
+    };
+    auto store = [&](int j, int buf) {
+      const int k0 = key_of(j);
+      u32x4* lk = reinterpret_cast<u32x4*>(group + buf * C::STAGE);
+      u32x4* lv = lk + C::TILE / 16;
+      const bool edge = k0 < kb || k0 + KT > ke;
+#pragma unroll
+      for (int i = 0; i < C::NL; ++i) {
+        const int c0 = i * C::GT + wr * 64;
+        if (C::CHUNKS % C::GT != 0 && c0 >= C::CHUNKS) break;
+        const int c = c0 + lane, r = c / C::CPR, col = c % C::CPR;
+        const bool none = edge && (k0 + r < kb || k0 + r >= ke);
+        const bool no_page = (bad >> i & 1) && !none;  // NaN scores for the rows that see it
+        const u32x4 zero = {0u, 0u, 0u, 0u}, nan = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+        if (none) rk[i] = zero;
+        if (none || no_page) rv[i] = zero;
+        if constexpr (C::QUANT) {
+          u32x4 lo, hi;
+          widen<C::CT>(rk[i], lo, hi);
+          if (no_page) lo = hi = nan;
+          lk[k_at<D>(r, 2 * col)] = lo, lk[k_at<D>(r, 2 * col + 1)] = hi;
+          widen<C::CT>(rv[i], lo, hi);
+          lv[v_at<D>(r, 2 * col)] = lo, lv[v_at<D>(r, 2 * col + 1)] = hi;
+        } else {
+          lk[k_at<D>(r, col)] = no_page ? nan : rk[i];
+          lv[v_at<D>(r, col)] = rv[i];
+        }
+      }
+      if constexpr (C::QUANT) {
+        float* ls = reinterpret_cast<float*>(group + buf * C::STAGE + 2 * C::TILE);
+#pragma unroll
+        for (int i = 0; i < C::NS; ++i) {
+          const int x = i * C::GT + gt;
+          if (x < 2 * KT) ls[x] = x < KT ? rs[i] * p.scale : rs[i];
+        }
+      }
+    };
+
+    f32x16 o[C::DB] = {};
+    float mx = kNegInf, l = 0.0f;
+    auto compute = [&](int j, int buf) {
+      const int k0 = key_of(j);
+      if (!wave_live || k0 > w_hi || k0 >= ke || (p.window > 0 && k0 + KT - 1 <= w_lo - p.window)) return;
+      const bf16x8* lk = reinterpret_cast<const bf16x8*>(group + buf * C::STAGE);
+      const unsigned char* lv = group + buf * C::STAGE + C::TILE;
+      const float* ls = reinterpret_cast<const float*>(group + buf * C::STAGE + 2 * C::TILE);
+      f32x16 x[C::KB] = {};
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i)
+#pragma unroll
+        for (int b = 0; b < C::KB; ++b)
+          x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lk[k_at<D>(32 * b + ql, 2 * i + hh)], qf[i], x[b], 0, 0, 0);
+      // ---- softmax
+      const bool masked = k0 + KT - 1 > w_lo || (p.window > 0 && k0 <= w_hi - p.window);
+#pragma unroll
+      for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float f[4] = {p.scale, p.scale, p.scale, p.scale};
+          if constexpr (C::QUANT) {
+            const float4 t = *reinterpret_cast<const float4*>(ls + 32 * b + 8 * g + 4 * hh);
+            f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= f[i];
+        }
+      if (masked) {
+#pragma unroll
+        for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int key = k0 + 32 * b + 8 * (e >> 2) + 4 * hh + (e & 3);
+            if ((unsigned)(key - vis0) >= (unsigned)vis_n) x[b][e] = kNegInf;
+          }
+      }
+      float top = x[0][0];
+#pragma unroll
+      for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[b][e]);
+      top = halves_max(top);
+      if (__any(top > mx + kSlack)) {
+        const float to = fmaxf(mx, top);
+        const float f = exp2_fast(mx - (to == kNegInf ? 0.0f : to));
+        mx = to;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < C::DB; ++d) o[d] *= f;
+      }
+      const float sub = mx == kNegInf ? 0.0f : mx;
+#pragma unroll
+      for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[b][e] = exp2_fast(x[b][e] - sub);
+          l += x[b][e];
+        }
+      if constexpr (C::QUANT) {
+#pragma unroll
+        for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 t = *reinterpret_cast<const float4*>(ls + KT + 32 * b + 8 * g + 4 * hh);
+            x[b][4 * g] *= t.x, x[b][4 * g + 1] *= t.y, x[b][4 * g + 2] *= t.z, x[b][4 * g + 3] *= t.w;
+          }
+      }
+      // ---- O += P V
+      const int tj = lane & 15;
+#pragma unroll
+      for (int b = 0; b < C::KB; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          u32x4 pk, pl;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p0 = x[b][8 * t + 2 * i], p1 = x[b][8 * t + 2 * i + 1];
+            pk[i] = cvt_bf16x2(p0, p1);
+            if constexpr (C::TERMS == 2)
+              pl[i] = cvt_bf16x2(p0 - __uint_as_float(pk[i] << 16), p1 - __uint_as_float(pk[i] & 0xffff0000u));
+          }
+          const bf16x8 pf = __builtin_bit_cast(bf16x8, pk);
+#pragma unroll
+          for (int d = 0; d < C::DB; ++d) {
+            const int r = 32 * b + 16 * t + 4 * hh + (tj >> 2), c = 4 * d + 2 * (lane >> 4 & 1) + (tj >> 1 & 1);
+            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_ptr)(lv + v_at<D>(r, c) * 16 + (tj & 1) * 8));
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_ptr)(lv + v_at<D>(r + 8, c) * 16 + (tj & 1) * 8));
+            const auto v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pf, o[d], 0, 0, 0);
+            if constexpr (C::TERMS == 2)
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
+                                                             __builtin_bit_cast(bf16x8, pl), o[d], 0, 0, 0);
+          }
+        }
+    };
+    // between LDS writes and reads of a tile: the waves that share it
+    auto sync = [&]() {
+      if constexpr (WR > 1)
+        __syncthreads();
+      else
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    if (nt > 0) {
+      issue(0);
+      store(0, 0);
+      if (nt > 1) issue(1);
+      sync();
+      for (int j = 0; j < nt; ++j) {
+        compute(j, C::NB == 2 ? j & 1 : 0);
+        if constexpr (C::NB == 1) sync();
+        if (j + 1 < nt) store(j + 1, C::NB == 2 ? (j + 1) & 1 : 0);
+        if (j + 2 < nt) issue(j + 2);
+        sync();
+      }
+    }
+    l = halves_sum(l);
+
+    // ---- rows whose O is not finite again, over their visible keys alone
+    {
+      bool fine = true;
+#pragma unroll
+      for (int d = 0; d < C::DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) fine = fine && fabsf(o[d][e]) < __builtin_inff();
+      const uint64_t b64 = __ballot(!fine);
+      unsigned rows = (unsigned)b64 | (unsigned)(b64 >> 32);
+      while (rows) {
+        const int rr = __ffs(rows) - 1;
+        rows &= rows - 1;
+        constexpr int E = D / 64;
+        const int r_tok = __builtin_amdgcn_readlane(tok, rr), r_head = __builtin_amdgcn_readlane(head, rr);
+        const int r_pos = __builtin_amdgcn_readlane(pos, rr), r_vis = __builtin_amdgcn_readlane(vis0, rr);
+        const uint16_t* qp = p.q + (q.q0 + r_tok) * p.q_ld + (int64_t)r_head * D;
+        float qv[E], ov[E], rm = kNegInf, rl = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) qv[e] = bf16_to_f32(qp[lane + 64 * e]), ov[e] = 0.0f;
+        for (int j = 0; j < nt; ++j) {
+          const int k0 = key_of(j);
+          for (int key = max(k0, r_vis); key < min(k0 + KT, r_pos + 1); ++key) {
+            const int page = page_of(key);
+            const bool none = (unsigned)page >= (unsigned)p.n_pages;
+            const int64_t at = (((int64_t)(none ? 0 : page) * p.Hkv + h) << p.page_shift) + (key & page_mask);
+            float d = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) d += qv[e] * cached<C::CT>(p.k_cache, at * D + lane + 64 * e);
+            d = wave_sum(d) * p.scale;
+            if (C::QUANT) d *= p.k_scale[at];
+            if (none) d = __builtin_nanf("");
+            const float to = fmaxf(rm, d), sub = to == kNegInf ? 0.0f : to;
+            const float f = exp2_fast(rm - sub), w = exp2_fast(d - sub);
+            rm = to, rl = rl * f + w;
+            const float wv = C::QUANT ? w * p.v_scale[at] : w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) ov[e] = ov[e] * f + wv * cached<C::CT>(p.v_cache, at * D + lane + 64 * e);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < C::DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at = 32 * d + 8 * (e >> 2) + 4 * hh + (e & 3);
+            const float v = __shfl(ov[d >> 1], at & 63);
+            if (ql == rr) o[d][e] = v;
+          }
+        if (ql == rr) mx = rm, l = rl;
+      }
+    }
+
+    // ---- to memory: blocks d0 .. d0 + nd - 1 of O (in v) of the lanes' rows
+    const bool to_slot = STREAM && !whole;
+    float* slot = STREAM ? slot_at<C>(p, 2 * blockIdx.x + (unit_lo == 0 ? 1 : 0)) : nullptr;
+    const int srow = wr * 32 + ql;  // row in the tile
+    auto put4 = [&](int d, const float* v, float inv) {  // elements d .. d + 3
+      if (to_slot) {
+        *reinterpret_cast<float4*>(slot + (size_t)srow * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+      } else if (live) {
+        *reinterpret_cast<u32x2*>(p.out + (q.q0 + tok) * p.out_ld + (int64_t)head * D + d) =
+            u32x2{cvt_bf16x2(v[0] * inv, v[1] * inv), cvt_bf16x2(v[2] * inv, v[3] * inv)};
+      }
+    };
+    auto put_sums = [&](float sm, float sl) {
+      if (hh != 0) return;
+      if (to_slot)
+        *reinterpret_cast<float2*>(slot + (size_t)C::R * D + 2 * srow) = make_float2(sm, sl);
+      else if (live && p.lse)
+        p.lse[(int64_t)(q.q0 + tok) * p.Hq + head] = sl > 0.0f || sl != sl ? (sm + log2f(sl)) * 0.6931471805599453f : kNegInf;
+    };
+    if constexpr (WK == 1) {
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      if (wave_live || to_slot) {
+#pragma unroll
+        for (int d = 0; d < C::DB; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float v[4] = {o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+            put4(32 * d + 8 * g + 4 * hh, v, inv);
+          }
+        put_sums(mx, l);
+      }
+      if (WR > 1 && STREAM) __syncthreads();  // the next item's first tile
+    } else {
+      // the waves' results of the same rows joined: each adds its share of the elements of all
+      float2* ml = reinterpret_cast<float2*>(smem + WK * C::NB * C::STAGE);  // [WK][32]
+      float* mine = reinterpret_cast<float*>(group);                        // [16 DB][64]
+      if (hh == 0) ml[wk * 32 + ql] = make_float2(mx, l);
+      __syncthreads();
+      float all = kNegInf, sum = 0.0f;
+      float2 part[WK];
+#pragma unroll
+      for (int w = 0; w < WK; ++w) part[w] = ml[w * 32 + ql], all = fmaxf(all, part[w].x);
+      const float sub = all == kNegInf ? 0.0f : all;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) sum += part[w].y * exp2_fast(part[w].x - sub);
+      const float f = exp2_fast(mx - sub);
+#pragma unroll
+      for (int d = 0; d < C::DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64 + lane] = o[d][e] * f;
+      __syncthreads();
+      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      constexpr int PER = C::DB * 4 / WK;  // groups of four registers a wave adds up
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int g4 = wk * PER + i;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < WK; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] += reinterpret_cast<const float*>(smem + w * C::NB * C::STAGE)[(4 * g4 + e) * 64 + lane];
+        put4(32 * (g4 >> 2) + 8 * (g4 & 3) + 4 * hh, v, inv);
+      }
+      if (wk == 0) put_sums(all, sum);
+      __syncthreads();  // before the next item's tiles
+    }
+    u += STREAM ? unit_hi - unit_lo : 1;
+  }
+}
+
+template <class C, bool STREAM>
+__global__ __launch_bounds__(C::THREADS, C::D == 256 ? 1 : 2) void attention_kernel(AttentionArgs p, int min_units) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  attention_body<C, STREAM>(p, min_units, smem);
+}
+
+// ---- host
+// How a call is cut, by its sizes alone.
+struct Plan {
+  bool few;     // up to 32 rows of a sequence: its keys are dealt over the waves of a workgroup
+  bool stream;  // equal shares of all keys instead of one workgroup per row tile
+  int grid, min_units, rows;
+};
+inline Plan plan_of(int T, int S, int Hq, int Hkv, int D, int64_t max_keys) {
+  const int64_t G = Hq / Hkv;
+  Plan p;
+  p.few = T * G <= 32 * (int64_t)S;
+  p.rows = p.few ? 32 : 128;
+  const int unit = p.few ? (D == 64 ? 256 : 128) : (D == 256 ? 32 : 64);
+  const int64_t tiles = T * G / p.rows + S;  // or fewer
+  const int64_t units = (max_keys + 63 + unit - 1) / unit;
+  const int64_t items = (T * G + p.rows - 1) / p.rows * Hkv;
+  p.min_units = p.few ? 1 : 4;
+  p.stream = p.few ? max_keys > 2 * unit : items < 384 && units > 2 * p.min_units;
+  const int64_t all = tiles * Hkv * (p.stream ? (units + p.min_units - 1) / p.min_units : 1);
+  const int64_t most = D == 256 ? 256 : 512;
+  p.grid = (int)(p.stream && all > most ? most : all);
+  return p;
+}
+
+// Joins the partial results of the items that more than one workgroup computed; grid and min_units as the launch
+// before, in x.  Workgroup w handles the item that begins in workgroup w's share and ends behind it.
+template <class C>
+__global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p, int min_units) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto weight = [&](int i) { return seq_work<C>(p, i); };
+  const int64_t total = sum_all(p.S, lane, weight);
+  const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
+  const int64_t u = blockIdx.x * per, u_end = u + per;
+  if (u_end >= total) return;
+  int64_t before;
+  const int s = __builtin_amdgcn_readfirstlane(find(p.S, lane, u_end - 1, weight, before));
+  const Seq q = seq_at(p, s);
+  const int units = seq_units<C>(p, q), tiles = row_tiles<C>(p, q);
+  const int64_t item = (u_end - 1 - before) / units, begin = before + item * units, end = begin + units;
+  if (begin < u || end <= u_end) return;
+  const int h = (int)(item / tiles), m = (int)(item - (int64_t)h * tiles);
+  const int n_rows = min(q.n * p.G - m * C::R, C::R);
+  const int first = (int)blockIdx.x, n = (int)((end - 1) / per) - first + 1;  // workgroups that hold a part
+  auto part = [&](int i) { return slot_at<C>(p, i == 0 ? 2 * first + 1 : 2 * (first + i)); };
+  constexpr int E = C::D / 64;
+  for (int r = blockIdx.y * 4 + wave; r < n_rows; r += gridDim.y * 4) {
+    float top = kNegInf;
+    for (int i = lane; i < n; i += 64) top = fmaxf(top, part(i)[C::R * C::D + 2 * r]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float sub = top == kNegInf ? 0.0f : top;
+    float sum = 0.0f, v[E] = {};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* a = part(i);
+      const float2 ml = *reinterpret_cast<const float2*>(a + (size_t)C::R * C::D + 2 * r);
+      const float f = exp2_fast(ml.x - sub);
+      sum += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += a[(size_t)r * C::D + lane * E + e] * f;
+    }
+    const int row = m * C::R + r, tok = row / p.G, head = h * p.G + row - tok * p.G;
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    uint16_t* out = p.out + (q.q0 + tok) * p.out_ld + (int64_t)head * C::D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = (uint16_t)cvt_bf16x2(v[e] * inv, 0.0f);
+    if (p.lse && lane == 0)
+      p.lse[(int64_t)(q.q0 + tok) * p.Hq + head] =
+          sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+  }
+}
+
+template <class C, bool STREAM>
+hipError_t run(const AttentionArgs& a, const Plan& plan, hipStream_t st) {
+  const auto kernel = attention_kernel<C, STREAM>;
+  // more than 64 KB of LDS has to be allowed once per device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    if (e != hipSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  kernel<<<plan.grid, C::THREADS, C::LDS, st>>>(a, plan.min_units);
+  if (STREAM && plan.grid > 1) combine_kernel<C><<<dim3(plan.grid, 4), 256, 0, st>>>(a, plan.min_units);
+  return hipGetLastError();
+}
+
+template <int D, int CT>
+hipError_t run_type(const AttentionArgs& a, const Plan& plan, hipStream_t st) {
+  using Few = Cfg<D, CT, 1, 4, D == 64 ? 64 : 32>;
+  using Many = Cfg<D, CT, 4, 1, D == 256 ? 32 : 64>;
+  if (plan.few) return plan.stream ? run<Few, true>(a, plan, st) : run<Few, false>(a, plan, st);
+  return plan.stream ? run<Many, true>(a, plan, st) : run<Many, false>(a, plan, st);
+}
+
+template <int CT>
+hipError_t run_all(const AttentionArgs& a, const Plan& plan, hipStream_t st) {
+  if (a.D == 64) return run_type<64, CT>(a, plan, st);
+  if (a.D == 128) return run_type<128, CT>(a, plan, st);
+  return run_type<256, CT>(a, plan, st);
+}
+
+hipError_t run_bf16(const AttentionArgs& a, const Plan& plan, hipStream_t st);
+hipError_t run_i8(const AttentionArgs& a, const Plan& plan, hipStream_t st);
+hipError_t run_e4m3(const AttentionArgs& a, const Plan& plan, hipStream_t st);
+
+}  // namespace attn
+}  // namespace moe

@@ -1,55 +1,10 @@
 // C ABI of the operators around the layer: argument checks, all before anything is enqueued.
-#include <stdarg.h>
-#include <stdio.h>
-#include <string.h>
-
-#include <atomic>
-
+#include "api_checks.h"
 #include "block_internal.h"
-#include "moe.h"
 
 using namespace moe;
 
 namespace {
-
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int code, const char* fmt, ...) {
-  char msg[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(msg, sizeof msg, fmt, ap);
-  va_end(ap);
-  return set_error(code, msg);
-}
-int ok() { return set_error(MOE_OK, ""); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Per-device cache of the architecture check: 0 unknown, 1 gfx950, 2 other.
-std::atomic<int> g_arch[64];
-
-int check_arch() {
-  int dev = -1;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(MOE_ERR_ARCH, "no HIP device: %s", hipGetErrorString(e));
-  if (dev < 0 || dev >= 64) return fail(MOE_ERR_ARCH, "device index %d out of range", dev);
-  int st = g_arch[dev].load(std::memory_order_relaxed);
-  if (st == 0) {
-    hipDeviceProp_t prop;
-    e = hipGetDeviceProperties(&prop, dev);
-    if (e != hipSuccess) return fail(MOE_ERR_ARCH, "hipGetDeviceProperties: %s", hipGetErrorString(e));
-    st = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-    g_arch[dev].store(st, std::memory_order_relaxed);
-  }
-  if (st != 1) return fail(MOE_ERR_ARCH, "device %d is not gfx950", dev);
-  return MOE_OK;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
 
 int check_rows(const char* f, int R) {
   if (R < 0 || R > kMaxProductRows) return fail(MOE_ERR_SHAPE, "%s: %d rows outside [0, 2^28]", f, R);
@@ -172,6 +127,24 @@ int moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, const fl
   p.a = a, p.b = b, p.a_scale = a_scale, p.b_scale = b_scale, p.bias = bias, p.add = add, p.a_div = 1;
   p.P = M, p.R = M, p.E = 1, p.N = N, p.Kb = K, p.c = c, p.c_f32 = c_type == MOE_F32;
   return hip_status(launch_product(p, true, (hipStream_t)stream), f);
+}
+
+int moe_gemm(const uint16_t* a, const uint16_t* b, const float* bias, int act, const uint16_t* add, int M, int N, int K,
+             void* c, int c_type, void* stream) {
+  const char* f = "moe_gemm";
+  int rc = check_product(f, N, K, 8, c_type);
+  if (rc || (rc = check_rows(f, M)) || (rc = check_out(f, M, N))) return rc;
+  if (act != MOE_ACT_NONE && act != MOE_ACT_SILU && act != MOE_ACT_GELU)
+    return fail(MOE_ERR_SHAPE, "%s: act=%d is no MOE_ACT_ value", f, act);
+  if (M == 0) return ok();
+  if (!a || !b || !c) return fail(MOE_ERR_NULL, "%s: a, b and c are required", f);
+  for (const void* q : {(const void*)a, (const void*)b, (const void*)bias, (const void*)add, (const void*)c})
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGN, "%s: tensors must be 16-byte aligned", f);
+  if ((rc = check_arch())) return rc;
+  ProductArgs p = {};
+  p.a = a, p.b = b, p.bias = bias, p.act = act, p.add = add, p.a_div = 1;
+  p.P = M, p.R = M, p.E = 1, p.N = N, p.Kb = 2 * K, p.c = c, p.c_f32 = c_type == MOE_F32;
+  return hip_status(launch_product(p, false, (hipStream_t)stream), f);
 }
 
 int moe_grouped_gemm(const uint16_t* a, const uint16_t* b, const int32_t* off, const int32_t* counts,

@@ -51,6 +51,7 @@ struct ProductArgs {
   const float* b_scale;   // per B row [E, N]
   const float* bias;      // dense: [N] or NULL
   const uint16_t* add;    // dense: [P, N] bf16 or NULL
+  int act;                // dense bf16: MOE_ACT_*
   const int32_t* off;     // [E + 1] first position of each expert; NULL: dense
   const int32_t* counts;  // [E] positions of each expert, NULL: off[e + 1] - off[e]
   const int32_t* rows;    // [P] output row of each position, NULL: the position itself

@@ -11,6 +11,7 @@
 #include <atomic>
 
 #include "block_internal.h"
+#include "moe.h"
 #include "product_rule.h"
 
 namespace moe {
@@ -22,10 +23,12 @@ typedef int i32x4v __attribute__((ext_vector_type(4)));
 template <bool I8>
 struct Acc {
   typedef f32x16 t32;
+  typedef f32x4 t16;
 };
 template <>
 struct Acc<true> {
   typedef i32x16 t32;
+  typedef i32x4v t16;
 };
 
 __device__ __forceinline__ f32x16 mma32(const u32x4& b, const u32x4& a, const f32x16& c) {
@@ -35,6 +38,28 @@ __device__ __forceinline__ f32x16 mma32(const u32x4& b, const u32x4& a, const f3
 __device__ __forceinline__ i32x16 mma32(const u32x4& b, const u32x4& a, const i32x16& c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4v, b), __builtin_bit_cast(i32x4v, a), c, 0, 0,
                                                0);
+}
+
+__device__ __forceinline__ f32x4 mma16(const u32x4& b, const u32x4& a, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ i32x4v mma16(const u32x4& b, const u32x4& a, const i32x4v& c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, b), __builtin_bit_cast(i32x4v, a), c, 0, 0,
+                                               0);
+}
+
+// What an epilogue does between the sum and the store: nothing, bias and addend, or an activation between the two.
+enum { kPlain = 0, kAdd = 1, kAct = 2 };
+
+// GELU in its tanh form: (1 + tanh z) / 2 = sigmoid(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3).
+__device__ __forceinline__ float activate(int act, float v) {
+  if (act == MOE_ACT_SILU) return silu(v);
+  if (act == MOE_ACT_GELU) {
+    const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-z2));
+  }
+  return v;
 }
 
 __device__ const u32x4 kZeros[1] = {{0u, 0u, 0u, 0u}};  // source of the chunks behind a row's end
@@ -108,7 +133,7 @@ __device__ __forceinline__ BlockAdd load_add(const ProductArgs& p, const BlockRo
 }
 
 // sa: the row's scale; sb, sbias: the block's 32 column scales and biases in LDS.  All lanes take part.
-template <bool I8, bool F32, bool EPI, class A>
+template <bool I8, bool F32, int EPI, class A>
 __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRows& r, float sa, const float* sb,
                                             const float* sbias, BlockAdd ad, int n, int lane, const A& acc) {
   const int h = lane >> 5;
@@ -133,8 +158,12 @@ __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRow
       const u32x4& w = g < 2 ? ad.lo : ad.hi;
       const uint32_t w0 = w[2 * (g & 1)], w1 = w[2 * (g & 1) + 1];
       const float4 b = *reinterpret_cast<const float4*>(sbias + 8 * g + 4 * h);
-      v[g][0] = v[g][0] + b.x + bf16_to_f32((uint16_t)w0), v[g][1] = v[g][1] + b.y + bf16_to_f32((uint16_t)(w0 >> 16));
-      v[g][2] = v[g][2] + b.z + bf16_to_f32((uint16_t)w1), v[g][3] = v[g][3] + b.w + bf16_to_f32((uint16_t)(w1 >> 16));
+      v[g][0] += b.x, v[g][1] += b.y, v[g][2] += b.z, v[g][3] += b.w;
+      if constexpr (EPI == kAct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[g][i] = activate(p.act, v[g][i]);
+      v[g][0] += bf16_to_f32((uint16_t)w0), v[g][1] += bf16_to_f32((uint16_t)(w0 >> 16));
+      v[g][2] += bf16_to_f32((uint16_t)w1), v[g][3] += bf16_to_f32((uint16_t)(w1 >> 16));
     }
     if constexpr (F32) {
       const int col = n + 8 * g + 4 * h;
@@ -159,17 +188,16 @@ __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRow
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// Few rows (dense 8-bit products): a workgroup owns 16 columns and reads their weights once, straight into
+// Few rows (dense products): a workgroup owns 16 columns and reads their weights once, straight into
 // registers.  Its four waves take every fourth 128-byte line of the rows (two 16 x 16 matrix instructions deep), U
 // lines at a time, and add their partial sums through LDS.  One row by 2048 x 4096 takes 3.2 us, a launch and one round
 // of loads; the bytes alone would take 1.8.
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-template <bool F32, bool EPI, int MT, int U>
+template <bool I8, bool F32, int EPI, int MT, int U>
 __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
   constexpr int W = 4;
-  __shared__ i32x4 part[W][MT][64];
+  typedef typename Acc<I8>::t16 acc_t;
+  __shared__ acc_t part[W][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = blockIdx.x * 16, k0 = (lane >> 4) * 16;
   const char* zeros = reinterpret_cast<const char*>(kZeros);
@@ -179,7 +207,7 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
   for (int m = 0; m < MT; ++m)
     a[m] = static_cast<const char*>(p.a) + (size_t)min(16 * m + (lane & 15), p.P - 1) * p.Kb;
   const int lines = (p.Kb + 127) / 128;
-  i32x4 acc[MT] = {};
+  acc_t acc[MT] = {};
   for (int l0 = wave; l0 < lines; l0 += W * U) {
     u32x4 fb[U][2], fa[MT][U][2];
 #pragma unroll
@@ -198,26 +226,31 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, fb[u][h]),
-                                                         __builtin_bit_cast(i32x4, fa[m][u][h]), acc[m], 0, 0, 0);
+          acc[m] = mma16(fb[u][h], fa[m][u][h], acc[m]);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
   __syncthreads();
   // wave m adds and stores row block m: lane l holds, of row l & 15, columns 4 (l >> 4) + i
   for (int m = wave; m < MT; m += W) {
-    const i32x4 s = (part[0][m][lane] + part[1][m][lane]) + (part[2][m][lane] + part[3][m][lane]);
+    const acc_t s = (part[0][m][lane] + part[1][m][lane]) + (part[2][m][lane] + part[3][m][lane]);
     const int id = 16 * m + (lane & 15), n = n0 + 4 * (lane >> 4);
     if (id >= p.P || n >= p.N) continue;
     const size_t at = (size_t)id * p.N + n;
-    const float sa = p.a_scale[id];
-    const float4 f = *reinterpret_cast<const float4*>(p.b_scale + n);
-    float v[4] = {(float)s[0] * sa * f.x, (float)s[1] * sa * f.y, (float)s[2] * sa * f.z, (float)s[3] * sa * f.w};
+    float v[4] = {(float)s[0], (float)s[1], (float)s[2], (float)s[3]};
+    if constexpr (I8) {
+      const float sa = p.a_scale[id];
+      const float4 f = *reinterpret_cast<const float4*>(p.b_scale + n);
+      v[0] = v[0] * sa * f.x, v[1] = v[1] * sa * f.y, v[2] = v[2] * sa * f.z, v[3] = v[3] * sa * f.w;
+    }
     if constexpr (EPI) {
       if (p.bias) {
         const float4 t = *reinterpret_cast<const float4*>(p.bias + n);
         v[0] += t.x, v[1] += t.y, v[2] += t.z, v[3] += t.w;
       }
+      if constexpr (EPI == kAct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = activate(p.act, v[i]);
       if (p.add) {
         const u32x2 w = *reinterpret_cast<const u32x2*>(p.add + at);
 #pragma unroll
@@ -362,7 +395,7 @@ struct ProductList {
   }
 };
 
-template <bool I8, bool EPI, int BM, int BN, int WM, int WN, int S>
+template <bool I8, int EPI, int BM, int BN, int WM, int WN, int S>
 struct RingCfg {
   static constexpr int NW = WM * WN, NT = NW * 64, MI = BM / WM / 32, NJ = BN / WN / 32;
   static constexpr int RPI = 64 / kCh;  // rows one load instruction fills
@@ -376,7 +409,7 @@ struct RingCfg {
   static_assert(BM % (RPI * NW) == 0 && BN % (RPI * NW) == 0 && BN <= NT && BM <= NT && LDS <= 160 * 1024, "");
 };
 
-template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
+template <bool I8, bool F32, int EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   using C = RingCfg<I8, EPI, BM, BN, WM, WN, S>;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -399,10 +432,10 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   int* s_ids = reinterpret_cast<int*>(smem + (size_t)S * C::STAGE * 16);  // [3][BM]
   float* s_sa = reinterpret_cast<float*>(s_ids + 3 * BM);                // [2][BM]
   float* s_sb = s_sa + 2 * BM;                                           // [2][BN]
-  float* s_bias = s_sb + 2 * BN;                                         // [2][BN]
+  float* s_bias = I8 ? s_sb + 2 * BN : s_sa;                             // [2][BN]
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
   const uint32_t lds_ids = lds0 + S * C::STAGE * 16, lds_sa = lds_ids + 3 * BM * 4;
-  const uint32_t lds_sb = lds_sa + 2 * BM * 4, lds_bias = lds_sb + 2 * BN * 4;
+  const uint32_t lds_sb = lds_sa + 2 * BM * 4, lds_bias = I8 ? lds_sb + 2 * BN * 4 : lds_sa;
 
   // at least S - 1 steps per item (those behind the row's end read zeros), so that an item's row ids have landed
   // when its loads begin and no buffer of an item is refilled before its epilogue
@@ -465,7 +498,10 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
       if (r < BN)
         to_lds4(p.b_scale + (size_t)lit.expert * p.N + min(lit.n0 + r, p.N - 1),
                 lds_sb + (uint32_t)(par * BN + wave * 64) * 4);
-      if (EPI && r < BN)
+    }
+    if constexpr (EPI != kPlain) {
+      const int par = l_index & 1, r = wave * 64 + lane;
+      if (r < BN)
         to_lds4(p.bias ? static_cast<const void*>(p.bias + min(lit.n0 + r, p.N - 1)) : kZeros,
                 lds_bias + (uint32_t)(par * BN + wave * 64) * 4);
     }
@@ -596,7 +632,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void ring_kernel(ProductArgs p) {
   wait_loads<0>();  // no load may reach LDS after the workgroup has ended
 }
 
-template <bool I8, bool F32, bool EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
+template <bool I8, bool F32, int EPI, bool NT, bool TAIL, int BM, int BN, int WM, int WN, int S>
 hipError_t ring_run(const ProductArgs& p, hipStream_t st) {
   using C = RingCfg<I8, EPI, BM, BN, WM, WN, S>;
   const auto kernel = ring_kernel<I8, F32, EPI, NT, TAIL, BM, BN, WM, WN, S>;
@@ -618,7 +654,7 @@ hipError_t ring_run(const ProductArgs& p, hipStream_t st) {
 
 // Rows that are whole steps, of which there are enough to fill the ring, and A offsets of 32 bits take the form
 // without tail handling (grouped bf16 prefill 367 against 375 us with it).
-template <bool I8, bool F32, bool EPI, bool NT, int BM, int BN, int WM, int WN, int S>
+template <bool I8, bool F32, int EPI, bool NT, int BM, int BN, int WM, int WN, int S>
 hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
   const int64_t a_rows = ((int64_t)p.R - 1) / p.a_div + 1;
   if (p.Kb % 128 == 0 && p.Kb / 128 >= S - 1 && a_rows * p.Kb <= ((int64_t)1 << 32))
@@ -628,7 +664,7 @@ hipError_t ring_launch(const ProductArgs& p, hipStream_t st) {
 
 ProductSize size_of(const ProductArgs& p) { return {p.P, p.R, p.E, p.N, p.Kb, p.off != nullptr}; }
 
-template <bool I8, bool F32, bool EPI, bool NT>
+template <bool I8, bool F32, int EPI, bool NT>
 hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
   switch (product_tile(size_of(p), NT)) {
     case 0:
@@ -640,28 +676,28 @@ hipError_t tiled_launch(const ProductArgs& p, hipStream_t st) {
   }
 }
 
-template <bool F32, bool EPI>
-hipError_t dense_i8_launch(const ProductArgs& p, hipStream_t st) {
+template <bool I8, bool F32, int EPI>
+hipError_t dense_launch(const ProductArgs& p, hipStream_t st) {
   // The few-rows kernel against the best tile, us (rows x K x columns): 1 x 2048 x 4096 3.2 against 6.1, 16 rows 3.9
   // against 6.2; 33 x 512 x 4096 3.5 against 4.0, 64 x 1024 x 4096 4.6 against 4.8, 48 x 2048 x 4096 6.2 against 6.3,
   // 64 rows 7.3 against 6.5, 33 x 4096 x 4096 11.1 against 9.5 (every workgroup reads all rows of A, and its loads
   // come in batches).  256 workgroups fill the CUs.
   const unsigned blocks = (unsigned)((p.N + 15) / 16);
   if (p.P <= 16) {
-    skinny_kernel<F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
+    skinny_kernel<I8, F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }
   if (p.P <= 64 && p.Kb <= 2048 && p.P * p.Kb <= 48 * 2048 && blocks <= 256) {
-    skinny_kernel<F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
+    skinny_kernel<I8, F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
     return hipGetLastError();
   }
-  return tiled_launch<true, F32, EPI, false>(p, st);
+  return tiled_launch<I8, F32, EPI, false>(p, st);
 }
 
 template <bool I8, bool F32>
 hipError_t grouped_launch(const ProductArgs& p, hipStream_t st) {
-  if (product_streams(size_of(p))) return tiled_launch<I8, F32, false, true>(p, st);
-  return tiled_launch<I8, F32, false, false>(p, st);
+  if (product_streams(size_of(p))) return tiled_launch<I8, F32, kPlain, true>(p, st);
+  return tiled_launch<I8, F32, kPlain, false>(p, st);
 }
 
 }  // namespace
@@ -675,10 +711,19 @@ hipError_t launch_product(const ProductArgs& args, bool i8, hipStream_t st) {
     p.div_mul = (unsigned)((1ull << (31 + l)) / (unsigned)p.a_div + 1);
     p.div_shift = l - 1;
   }
-  if (!i8) return p.c_f32 ? grouped_launch<false, true>(p, st) : grouped_launch<false, false>(p, st);
-  if (p.off) return p.c_f32 ? grouped_launch<true, true>(p, st) : grouped_launch<true, false>(p, st);
-  if (p.bias || p.add) return p.c_f32 ? dense_i8_launch<true, true>(p, st) : dense_i8_launch<false, true>(p, st);
-  return p.c_f32 ? dense_i8_launch<true, false>(p, st) : dense_i8_launch<false, false>(p, st);
+  if (p.off) {
+    if (!i8) return p.c_f32 ? grouped_launch<false, true>(p, st) : grouped_launch<false, false>(p, st);
+    return p.c_f32 ? grouped_launch<true, true>(p, st) : grouped_launch<true, false>(p, st);
+  }
+  const bool add = p.bias || p.add;
+  if (i8) {
+    if (add) return p.c_f32 ? dense_launch<true, true, kAdd>(p, st) : dense_launch<true, false, kAdd>(p, st);
+    return p.c_f32 ? dense_launch<true, true, kPlain>(p, st) : dense_launch<true, false, kPlain>(p, st);
+  }
+  if (p.act != MOE_ACT_NONE)
+    return p.c_f32 ? dense_launch<false, true, kAct>(p, st) : dense_launch<false, false, kAct>(p, st);
+  if (add) return p.c_f32 ? dense_launch<false, true, kAdd>(p, st) : dense_launch<false, false, kAdd>(p, st);
+  return p.c_f32 ? dense_launch<false, true, kPlain>(p, st) : dense_launch<false, false, kPlain>(p, st);
 }
 
 }  // namespace moe

@@ -33,10 +33,23 @@ EXPORTS = (
     "moe_align", "moe_grouped_gate_up", "moe_grouped_down", "moe_combine", "moe_forward_fp8", "moe_e4m3_to_f32", "moe_forward_q4",
     "moe_bucket_plan", "moe_prefill_runner_create", "moe_prefill_runner_create_fp8", "moe_prefill_runner_run", "moe_prefill_runner_destroy",
     "moe_forward_noalloc", "moe_workspace_sections",
-    "moe_block_norm", "moe_quantize_i8", "moe_swiglu_i8", "moe_gemm_i8", "moe_grouped_gemm", "moe_grouped_gemm_i8",
+    "moe_block_norm", "moe_quantize_i8", "moe_swiglu_i8", "moe_gemm_i8", "moe_gemm", "moe_grouped_gemm", "moe_grouped_gemm_i8",
+    "moe_rope_frequencies", "moe_rope", "moe_cache_write", "moe_cache_read", "moe_attention_workspace_size",
+    "moe_attention",
 )
 BF16 = 0  # MOE_BF16, MOE_F32: types of a residual stream and of a product's output
 F32 = 1
+I8 = 2  # MOE_I8, MOE_E4M3: types of a cache, beside BF16
+E4M3 = 3
+ROPE_HALF = 0  # MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED: which elements a rotation pairs
+ROPE_INTERLEAVED = 1
+ROPE_PLAIN = 0  # MOE_ROPE_*: scalings of the rotations' frequencies
+ROPE_LINEAR = 1
+ROPE_NTK = 2
+ROPE_YARN = 3
+ACT_NONE = 0  # MOE_ACT_*: activations of moe_gemm's epilogue
+ACT_SILU = 1
+ACT_GELU = 2
 NOALLOC_WS_BYTES = 64 << 20  # MOE_NOALLOC_WS_BYTES: the fixed workspace of moe_forward_noalloc
 
 
@@ -56,7 +69,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with `python -m sparse_moe_layer_03_amd.build`")
         L = C.CDLL(LIB_PATH)
-        p, i, z, i64, f = C.c_void_p, C.c_int, C.c_size_t, C.c_int64, C.c_float
+        p, i, z, i64, f, d = C.c_void_p, C.c_int, C.c_size_t, C.c_int64, C.c_float, C.c_double
         sig = {
             "moe_status_str": ([i], C.c_char_p),
             "moe_last_error": ([], C.c_char_p),
@@ -90,9 +103,18 @@ def lib():
             "moe_quantize_i8": ([p, i, i, p, p, p], i),
             "moe_swiglu_i8": ([p, p, i, i, p, p, p], i),
             "moe_gemm_i8": ([p] * 6 + [i] * 3 + [p, i, p], i),
+            "moe_gemm": ([p, p, p, i, p] + [i] * 3 + [p, i, p], i),
             "moe_grouped_gemm": ([p] * 5 + [i] * 6 + [p, i, p], i),
             "moe_grouped_gemm_i8": ([p] * 7 + [i] * 6 + [p, i, p], i),
         }
+        sig.update({
+            "moe_rope_frequencies": ([i, d, i, d, d, p, p], i),
+            "moe_rope": ([p, i64, p, f, f, p, p, f] + [i] * 5 + [p, i64, p], i),
+            "moe_cache_write": ([p, i64, p, p, i64, p, i64, p, p, i64, f, f, p, p, f, p] + [i] * 9 + [p] * 5, i),
+            "moe_cache_read": ([p] * 4 + [i] * 3 + [p] + [i] * 3 + [p, p, i, p], i),
+            "moe_attention_workspace_size": ([i] * 5 + [i64], z),
+            "moe_attention": ([p, i64] + [p] * 4 + [i] + [p] * 3 + [i] * 8 + [f, i, p, i64, p, p, z, p], i),
+        })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -420,6 +442,16 @@ def moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, stream=None):
     _check(lib().moe_gemm_i8(a, a_scale, b, b_scale, bias, add, M, N, K, c, c_type, _stream(stream)))
 
 
+def moe_gemm(a, b, bias, add, M, N, K, c, act: int = ACT_NONE, stream=None):
+    """The type of c (bf16 or fp32) is the output's."""
+    import torch
+    bf = torch.bfloat16
+    c_type, ct = _type("c", c)
+    a, b, bias, add, c = _args(("a", a, bf, (M, K)), ("b", b, bf, (N, K)), ("bias", bias, torch.float32, (N,)),
+                               ("add", add, bf, (M, N)), ("c", c, ct, (M, N)))
+    _check(lib().moe_gemm(a, b, bias, act, add, M, N, K, c, c_type, _stream(stream)))
+
+
 def _a_rows(a_div, R):
     return (R - 1) // a_div + 1 if R > 0 and a_div > 0 else 0
 
@@ -447,3 +479,109 @@ def moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, 
         ("rows", rows, i32, (P,)), ("c", c, ct, (R, N)))
     _check(lib().moe_grouped_gemm_i8(a, a_scale, b, b_scale, off, counts, rows, a_div, P, R, E, N, K, c, c_type,
                                      _stream(stream)))
+
+
+# ------------------------------------------------------------- operators around attention
+def _rows(name, t, n, width):
+    """(pointer, elements from row to row) of n rows of `width` bf16 elements: a tensor whose rows are whole (the part
+    of a wider matrix's columns, say) or one that _args takes for [n, width].  Raw pointers stand for rows without
+    gaps."""
+    import torch
+    if t is None or t.__class__ is int:
+        return t, width
+    if (t.dtype is torch.bfloat16 and t.dim() > 1 and t.shape[0] >= n > 0 and math.prod(t.shape[1:]) == width
+            and t[0].is_contiguous()):
+        at = t.get_device()
+        if at < 0:
+            raise ValueError(f"{name} is on {t.device}, not on a GPU")
+        if at != _device():
+            raise ValueError(f"{name} is on GPU {at}; the current one is {_device()}")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+    return _args((name, t, torch.bfloat16, (n, width)))[0], width
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D):
+    """(MOE_ type, pointers) of a cache, whose type is its tensors'."""
+    import torch
+    types = {torch.bfloat16: BF16, torch.int8: I8, torch.float8_e4m3fn: E4M3}
+    if k_cache is None or k_cache.__class__ is int:
+        raise ValueError("k_cache must be a tensor: its type is the call's")
+    if k_cache.dtype not in types:
+        raise ValueError(f"k_cache is {k_cache.dtype}; expected {', '.join(map(str, types))}")
+    shape = (n_pages, Hkv, P, D)
+    return types[k_cache.dtype], _args(
+        ("k_cache", k_cache, k_cache.dtype, shape), ("v_cache", v_cache, k_cache.dtype, shape),
+        ("k_scale", k_scale, torch.float32, shape[:3]), ("v_scale", v_scale, torch.float32, shape[:3]))
+
+
+def moe_rope_frequencies(rot: int, base: float, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                         original: float = 0.0, device=None):
+    """(freq [rot / 2] float64, on ``device`` if given, mscale) as moe_rope takes them."""
+    import torch
+    freq = torch.empty(max(rot // 2, 0), dtype=torch.float64)
+    mscale = C.c_float(0.0)
+    _check(lib().moe_rope_frequencies(rot, base, scaling, factor, original, freq.data_ptr(), C.byref(mscale)))
+    return freq if device is None else freq.to(device), mscale.value
+
+
+def moe_rope(x, w_norm, pos, freq, T, heads, D, rot, pairs, out, mscale: float = 1.0, w_add: float = 0.0,
+             eps: float = 1e-6, stream=None):
+    """x and out may be columns of wider rows; out may be x."""
+    import torch
+    x, x_ld = _rows("x", x, T, heads * D)
+    out, out_ld = _rows("out", out, T, heads * D)
+    w_norm, pos, freq = _args(("w_norm", w_norm, torch.bfloat16, (D,)), ("pos", pos, torch.int32, (T,)),
+                              ("freq", freq, torch.float64, (rot // 2,)))
+    _check(lib().moe_rope(x, x_ld, w_norm, w_add, eps, pos, freq, mscale, T, heads, D, rot, pairs, out, out_ld,
+                          _stream(stream)))
+
+
+def moe_cache_write(q, w_q, q_out, k, w_k, v, pos, freq, slots, T, Hq, Hkv, D, rot, pairs, k_cache, v_cache, k_scale,
+                    v_scale, n_pages, P, mscale: float = 1.0, w_add: float = 0.0, eps: float = 1e-6, stream=None):
+    """The type of k_cache (bfloat16, int8 or float8_e4m3fn) is the cache's; q, q_out, k and v may be columns of wider
+    rows."""
+    import torch
+    q, q_ld = _rows("q", q, T, Hq * D)
+    q_out, q_out_ld = _rows("q_out", q_out, T, Hq * D)
+    k, k_ld = _rows("k", k, T, Hkv * D)
+    v, v_ld = _rows("v", v, T, Hkv * D)
+    cache_type, cache = _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D)
+    bf, i32 = torch.bfloat16, torch.int32
+    w_q, w_k, pos, freq, slots = _args(("w_q", w_q, bf, (D,)), ("w_k", w_k, bf, (D,)), ("pos", pos, i32, (T,)),
+                                       ("freq", freq, torch.float64, (rot // 2,)), ("slots", slots, i32, (T,)))
+    _check(lib().moe_cache_write(q, q_ld, w_q, q_out, q_out_ld, k, k_ld, w_k, v, v_ld, w_add, eps, pos, freq, mscale,
+                                 slots, T, Hq, Hkv, D, rot, pairs, cache_type, n_pages, P, *cache, _stream(stream)))
+
+
+def moe_cache_read(k_cache, v_cache, k_scale, v_scale, slots, n, Hkv, D, n_pages, P, k, v, stream=None):
+    """The type of k (bf16 or fp32) is the output's, that of k_cache the cache's."""
+    import torch
+    out_type, ot = _type("k", k)
+    cache_type, cache = _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D)
+    slots, k, v = _args(("slots", slots, torch.int32, (n,)), ("k", k, ot, (n, Hkv, D)), ("v", v, ot, (n, Hkv, D)))
+    _check(lib().moe_cache_read(*cache, cache_type, n_pages, P, slots, n, Hkv, D, k, v, out_type, _stream(stream)))
+
+
+def moe_attention_workspace_size(T: int, S: int, Hq: int, Hkv: int, D: int, max_keys: int) -> int:
+    return lib().moe_attention_workspace_size(T, S, Hq, Hkv, D, max_keys)
+
+
+def moe_attention(q, k_cache, v_cache, k_scale, v_scale, pages, q_start, kv_len, T, S, Hq, Hkv, D, n_pages, P,
+                  max_pages, out, workspace, scale: Optional[float] = None, window: int = 0, lse=None, stream=None):
+    """The type of k_cache is the cache's; q and out may be columns of wider rows.  workspace: a tensor of
+    moe_attention_workspace_size bytes or more, None where that is 0.  scale: None for D ** -0.5."""
+    import torch
+    q, q_ld = _rows("q", q, T, Hq * D)
+    out, out_ld = _rows("out", out, T, Hq * D)
+    cache_type, cache = _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D)
+    if workspace.__class__ is int:
+        raise ValueError("workspace must be a tensor: its size is read")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    i32 = torch.int32
+    pages, q_start, kv_len, lse, ws = _args(
+        ("pages", pages, i32, (S, max_pages)), ("q_start", q_start, i32, (S + 1,)), ("kv_len", kv_len, i32, (S,)),
+        ("lse", lse, torch.float32, (T, Hq)),
+        ("workspace", workspace, None if workspace is None else workspace.dtype, (0,)))
+    _check(lib().moe_attention(q, q_ld, *cache, cache_type, pages, q_start, kv_len, T, S, Hq, Hkv, D, n_pages, P,
+                               max_pages, D ** -0.5 if scale is None else scale, window, out, out_ld, lse, ws, ws_bytes,
+                               _stream(stream)))
