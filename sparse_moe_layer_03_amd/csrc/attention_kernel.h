@@ -44,9 +44,12 @@ struct Cfg {
   static constexpr int NL = (CHUNKS + GT - 1) / GT;
   static constexpr int NS = QUANT ? (2 * KT + GT - 1) / GT : 1;  // scales a thread loads
   static constexpr int NB = WR == 1 ? 1 : 2;   // tiles in LDS: a wave alone needs no second one
-  static constexpr int TILE = KT * D * 2;      // bytes of a tile's K or V in LDS, bf16
+  // Bytes from row to row in LDS, bf16.  A K read takes one 16-byte chunk of 32 rows: 16 rows in a row lie in different
+  // banks.  A transposing V read takes four rows of 64 bytes, which do so likewise.
+  static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 64;
   static constexpr int SCALES = QUANT ? 2 * KT * 4 : 0;
-  static constexpr int STAGE = 2 * TILE + SCALES;
+  static constexpr int STAGE = KT * (KROW + VROW) + SCALES;
+  static constexpr int NP = WR == 1 ? KT / 16 : NL;  // page numbers a wave looks up per tile
   static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
@@ -58,11 +61,15 @@ struct Cfg {
 struct Seq {
   int q0, n, len;  // first row of q, new tokens, keys
 };
+// PTR: how q_start and kv_len are read, by lanes of their own or (s the same in all) by scalar loads.
+typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+template <class PTR>
 __device__ __forceinline__ Seq seq_at(const AttentionArgs& p, int s) {
+  const PTR start = (PTR)(uintptr_t)p.q_start, len = (PTR)(uintptr_t)p.kv_len;
   Seq q;
-  q.q0 = min(max(p.q_start[s], 0), p.T);
-  q.n = max(min(max(p.q_start[s + 1], 0), p.T) - q.q0, 0);
-  q.len = min(max(p.kv_len[s], 0), p.max_pages << p.page_shift);
+  q.q0 = min(max(start[s], 0), p.T);
+  q.n = max(min(max(start[s + 1], 0), p.T) - q.q0, 0);
+  q.len = min(max(len[s], 0), p.max_pages << p.page_shift);
   return q;
 }
 // First key that any of the sequence's rows sees, down to a multiple of 64: where its units begin.
@@ -80,7 +87,7 @@ __device__ __forceinline__ int row_tiles(const AttentionArgs& p, const Seq& q) {
 // Units of work of a sequence: all its row tiles and key heads times its keys.
 template <class C>
 __device__ __forceinline__ int64_t seq_work(const AttentionArgs& p, int s) {
-  const Seq q = seq_at(p, s);
+  const Seq q = seq_at<const int32_t*>(p, s);
   return (int64_t)p.Hkv * row_tiles<C>(p, q) * seq_units<C>(p, q);
 }
 
@@ -92,12 +99,16 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
   }
   return v;
 }
+__device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 // Sum of weight(s) over all sequences.
 template <class W>
 __device__ __forceinline__ int64_t sum_all(int S, int lane, W weight) {
   int64_t sum = 0;
   for (int b = 0; b < S; b += 64) sum += b + lane < S ? weight(b + lane) : 0;
-  return __shfl(wave_scan(sum, lane), 63);
+  return lane_value(wave_scan(sum, lane), 63);
 }
 // The sequence in which the running sum of weights passes `at`, and the sum before it; S if none does.
 template <class W>
@@ -107,10 +118,10 @@ __device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64
     const int64_t incl = before + wave_scan(b + lane < S ? weight(b + lane) : 0, lane);
     const int n = __popcll(__ballot(incl <= at));
     if (n < 64) {
-      if (n > 0) before = __shfl(incl, n - 1);
+      if (n > 0) before = lane_value(incl, n - 1);
       return b + n;
     }
-    before = __shfl(incl, 63);
+    before = lane_value(incl, 63);
   }
   return S;
 }
@@ -126,19 +137,6 @@ __device__ __forceinline__ float halves_sum(float v) {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// 16-byte chunk c of row r of a tile in LDS.  K: a read takes one chunk of 16 and more consecutive rows.  V: a
-// transposing read takes four rows of two neighbouring chunks.
-template <int D>
-__device__ __forceinline__ int k_at(int r, int c) {
-  if constexpr (D == 64) return r * 8 + (c ^ (((r >> 1) ^ ((r & 1) << 2)) & 7));
-  return r * (D / 8) + (c ^ (r & 15));
-}
-template <int D>
-__device__ __forceinline__ int v_at(int r, int c) {
-  if constexpr (D == 64) return r * 8 + (c ^ (((r >> 1) & 1) << 2));
-  return r * (D / 8) + (c ^ ((r & 3) << 2));
-}
 
 // Sixteen codes as two chunks of bf16 (every code is one exactly).
 template <int CT>
@@ -194,7 +192,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     if (u >= u_end) return;
     s = find(p.S, lane, u, weight, before);
   } else {
-    auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at(p, i)); };
+    auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at<const int32_t*>(p, i)); };
     // the last tiles, which see the most keys, first
     const int64_t tiles = gridDim.x / p.Hkv;
     h = blockIdx.x % p.Hkv;
@@ -202,10 +200,9 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     if (s >= p.S) return;
     m = (int)(tiles - 1 - blockIdx.x / p.Hkv - before);
   }
-  s = __builtin_amdgcn_readfirstlane(s);
 
   while (u < u_end) {
-    const Seq q = seq_at(p, s);
+    const Seq q = seq_at<scalar_ptr>(p, s);
     const int units = seq_units<C>(p, q), base = seq_base(p, q);
     int unit_lo = 0, unit_hi = units;
     if constexpr (STREAM) {
@@ -252,27 +249,40 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     const int u_last = ke > kb ? min(unit_hi, (ke - base + C::UNIT - 1) / C::UNIT) : 0;
     const int nt = max(u_last - u_first, 0);
     auto key_of = [&](int j) { return base + ((u_first + j) * WK + wk) * KT; };
-    const int32_t* pages = p.pages + (int64_t)s * p.max_pages;
+    const scalar_ptr pages = (scalar_ptr)(uintptr_t)(p.pages + (int64_t)s * p.max_pages);
     const int page_mask = (1 << p.page_shift) - 1;
+    // the page of a key, or of the nearest key that the rows see
+    auto page_of = [&](int key) { return pages[min(max(key, kb), ke - 1) >> p.page_shift]; };
 
     u32x4 rk[C::NL], rv[C::NL];
     float rs[C::NS];
-    unsigned bad = 0;  // bit i: load i's page is none
-    auto page_of = [&](int key) { return pages[min(max(key, kb), ke - 1) >> p.page_shift]; };
-    // the 64 lanes of a load read rows of one page: they begin at a multiple of, and are at most, 16
+    unsigned bad = 0;   // bit i: page i is none
+    int page[C::NP];    // of the next tile: a scalar load's latency ahead
+    // The 64 lanes of a load read rows of one page: they begin at a multiple of, and are at most, 16.  lookup(i): which
+    // of the wave's page numbers load i takes; first_row(i): its first row.
+    auto lookup = [&](int i) { return WR == 1 ? i * 64 / C::CPR / 16 : i; };
+    auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
+    auto look_up = [&](int j) {
+      const int k0 = key_of(j);
+#pragma unroll
+      for (int i = 0; i < C::NP; ++i) page[i] = page_of(k0 + (WR == 1 ? 16 * i : first_row(i)));
+    };
     auto issue = [&](int j) {
       const int k0 = key_of(j);
       bad = 0;
+      int64_t row[C::NP];  // first row of the page's part
+#pragma unroll
+      for (int i = 0; i < C::NP; ++i) {
+        int n = page[i];
+        if ((unsigned)n >= (unsigned)p.n_pages) n = 0, bad |= 1u << i;
+        row[i] = ((int64_t)n * p.Hkv + h) << p.page_shift;
+      }
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
-        const int c0 = i * C::GT + wr * 64;
-        if (C::CHUNKS % C::GT != 0 && c0 >= C::CHUNKS) break;
-        const int key = k0 + c0 / C::CPR;
-        int page = page_of(key);
-        if ((unsigned)page >= (unsigned)p.n_pages) page = 0, bad |= 1u << i;
-        const int64_t at = ((((int64_t)page * p.Hkv + h) << p.page_shift) + (key & page_mask)) * C::ROWB + lane * 16;
-        rk[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k_cache) + at);
-        rv[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.v_cache) + at);
+        if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
+        const int64_t at = (row[lookup(i)] + ((k0 + first_row(i)) & page_mask)) * C::ROWB;
+        rk[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k_cache) + at + lane * 16);
+        rv[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.v_cache) + at + lane * 16);
       }
       if constexpr (C::QUANT) {
 #pragma unroll
@@ -280,43 +290,46 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           const int x = i * C::GT + gt, key = k0 + x % KT;
           rs[i] = 0.0f;
           if (x < 2 * KT && key >= kb && key < ke) {
-            const int page = page_of(key);
-            if ((unsigned)page < (unsigned)p.n_pages)
-              rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)page * p.Hkv + h) << p.page_shift) +
-                                                       (key & page_mask)];
+            const int n = p.pages[(int64_t)s * p.max_pages + (key >> p.page_shift)];
+            if ((unsigned)n < (unsigned)p.n_pages)
+              rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)n * p.Hkv + h) << p.page_shift) + (key & page_mask)];
           }
         }
       }
+      if (j + 1 < nt) look_up(j + 1);
     };
+    // this lane's place of load i
+    const int c_lane = (wr * 64 + lane) % C::CPR, r_lane = (wr * 64 + lane) / C::CPR;
     auto store = [&](int j, int buf) {
       const int k0 = key_of(j);
-      u32x4* lk = reinterpret_cast<u32x4*>(group + buf * C::STAGE);
-      u32x4* lv = lk + C::TILE / 16;
+      unsigned char* lk = group + buf * C::STAGE;
+      unsigned char* lv = lk + KT * C::KROW;
       const bool edge = k0 < kb || k0 + KT > ke;
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
-        const int c0 = i * C::GT + wr * 64;
-        if (C::CHUNKS % C::GT != 0 && c0 >= C::CHUNKS) break;
-        const int c = c0 + lane, r = c / C::CPR, col = c % C::CPR;
+        if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
+        const int r = r_lane + i * (C::GT / C::CPR);
         const bool none = edge && (k0 + r < kb || k0 + r >= ke);
-        const bool no_page = (bad >> i & 1) && !none;  // NaN scores for the rows that see it
+        const bool no_page = (bad >> lookup(i) & 1) && !none;  // NaN scores for the rows that see it
         const u32x4 zero = {0u, 0u, 0u, 0u}, nan = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
         if (none) rk[i] = zero;
         if (none || no_page) rv[i] = zero;
+        u32x4* tk = reinterpret_cast<u32x4*>(lk + r * C::KROW + c_lane * (C::QUANT ? 32 : 16));
+        u32x4* tv = reinterpret_cast<u32x4*>(lv + r * C::VROW + c_lane * (C::QUANT ? 32 : 16));
         if constexpr (C::QUANT) {
           u32x4 lo, hi;
           widen<C::CT>(rk[i], lo, hi);
           if (no_page) lo = hi = nan;
-          lk[k_at<D>(r, 2 * col)] = lo, lk[k_at<D>(r, 2 * col + 1)] = hi;
+          tk[0] = lo, tk[1] = hi;
           widen<C::CT>(rv[i], lo, hi);
-          lv[v_at<D>(r, 2 * col)] = lo, lv[v_at<D>(r, 2 * col + 1)] = hi;
+          tv[0] = lo, tv[1] = hi;
         } else {
-          lk[k_at<D>(r, col)] = no_page ? nan : rk[i];
-          lv[v_at<D>(r, col)] = rv[i];
+          tk[0] = no_page ? nan : rk[i];
+          tv[0] = rv[i];
         }
       }
       if constexpr (C::QUANT) {
-        float* ls = reinterpret_cast<float*>(group + buf * C::STAGE + 2 * C::TILE);
+        float* ls = reinterpret_cast<float*>(lv + KT * C::VROW);
 #pragma unroll
         for (int i = 0; i < C::NS; ++i) {
           const int x = i * C::GT + gt;
@@ -330,15 +343,16 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     auto compute = [&](int j, int buf) {
       const int k0 = key_of(j);
       if (!wave_live || k0 > w_hi || k0 >= ke || (p.window > 0 && k0 + KT - 1 <= w_lo - p.window)) return;
-      const bf16x8* lk = reinterpret_cast<const bf16x8*>(group + buf * C::STAGE);
-      const unsigned char* lv = group + buf * C::STAGE + C::TILE;
-      const float* ls = reinterpret_cast<const float*>(group + buf * C::STAGE + 2 * C::TILE);
+      const unsigned char* lk = group + buf * C::STAGE + ql * C::KROW + hh * 16;
+      const unsigned char* lv = group + buf * C::STAGE + KT * C::KROW;
+      const float* ls = reinterpret_cast<const float*>(lv + KT * C::VROW);
       f32x16 x[C::KB] = {};
 #pragma unroll
       for (int i = 0; i < C::NQ; ++i)
 #pragma unroll
         for (int b = 0; b < C::KB; ++b)
-          x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lk[k_at<D>(32 * b + ql, 2 * i + hh)], qf[i], x[b], 0, 0, 0);
+          x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              *reinterpret_cast<const bf16x8*>(lk + 32 * b * C::KROW + 32 * i), qf[i], x[b], 0, 0, 0);
       // ---- softmax
       const bool masked = k0 + KT - 1 > w_lo || (p.window > 0 && k0 <= w_hi - p.window);
 #pragma unroll
@@ -394,7 +408,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           }
       }
       // ---- O += P V
-      const int tj = lane & 15;
+      // lane j of 16 reads row j / 4, elements 4 (j % 4) .. + 3, and gets element j of the four rows
+      const unsigned char* tv = lv + (4 * hh + (lane >> 2 & 3)) * C::VROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
@@ -410,12 +425,10 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           const bf16x8 pf = __builtin_bit_cast(bf16x8, pk);
 #pragma unroll
           for (int d = 0; d < C::DB; ++d) {
-            const int r = 32 * b + 16 * t + 4 * hh + (tj >> 2), c = 4 * d + 2 * (lane >> 4 & 1) + (tj >> 1 & 1);
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(lv + v_at<D>(r, c) * 16 + (tj & 1) * 8));
-            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(lv + v_at<D>(r + 8, c) * 16 + (tj & 1) * 8));
+            const unsigned char* at = tv + (32 * b + 16 * t) * C::VROW + 64 * d;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 8 * C::VROW));
             const auto v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pf, o[d], 0, 0, 0);
             if constexpr (C::TERMS == 2)
@@ -432,6 +445,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     if (nt > 0) {
+      look_up(0);
       issue(0);
       store(0, 0);
       if (nt > 1) issue(1);
@@ -609,8 +623,8 @@ __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p, int min_u
   const int64_t u = blockIdx.x * per, u_end = u + per;
   if (u_end >= total) return;
   int64_t before;
-  const int s = __builtin_amdgcn_readfirstlane(find(p.S, lane, u_end - 1, weight, before));
-  const Seq q = seq_at(p, s);
+  const int s = find(p.S, lane, u_end - 1, weight, before);
+  const Seq q = seq_at<scalar_ptr>(p, s);
   const int units = seq_units<C>(p, q), tiles = row_tiles<C>(p, q);
   const int64_t item = (u_end - 1 - before) / units, begin = before + item * units, end = begin + units;
   if (begin < u || end <= u_end) return;
