@@ -29,6 +29,19 @@ constexpr float kNegInf = -__builtin_inff();
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// LDS by its own 32-bit addresses: constant distances become the instructions' offsets.
+#define MOE_LDS __attribute__((address_space(3)))
+typedef MOE_LDS unsigned char* lds_bytes;
+template <class T>
+__device__ __forceinline__ MOE_LDS T* lds_as(lds_bytes p) {
+  return (MOE_LDS T*)p;
+}
+// A value that is worked out anew behind this point, not kept in a register from before a loop.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // D: head elements; CT: type of the cache; WR waves of 32 rows share a tile of KT keys; WK waves take every WK-th tile.
 template <int D_, int CT_, int WR_, int WK_, int KT_>
 struct Cfg {
@@ -48,7 +61,9 @@ struct Cfg {
   // banks.  A transposing V read takes four rows of 64 bytes, which do so likewise.
   static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 64;
   static constexpr int SCALES = QUANT ? 2 * KT * 4 : 0;
-  static constexpr int STAGE = KT * (KROW + VROW) + SCALES;
+  static constexpr bool KREG = WR == 1;  // K goes from memory into the operand registers
+  static constexpr int KTILE = KREG ? 0 : KT * KROW;
+  static constexpr int STAGE = (KTILE + KT * VROW > 32 * D * 4 || WK == 1 ? KTILE + KT * VROW : 32 * D * 4) + SCALES;
   static constexpr int NP = WR == 1 ? KT / 16 : NL;  // page numbers a wave looks up per tile
   static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
@@ -173,30 +188,29 @@ __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
 // may begin and end inside such an item: what is not a whole item goes to the workspace, slot 2 w for the end of an item
 // and 2 w + 1 for a beginning, and combine_kernel joins it.
 template <class C, bool STREAM>
-__device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, unsigned char* smem) {
+__device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, lds_bytes smem) {
   constexpr int D = C::D, KT = C::KT, WR = C::WR, WK = C::WK;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = wave % WR, wk = wave / WR, gt = tid % C::GT;
-  const int hh = lane >> 5, ql = lane & 31;
+  const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave % WR, wk = wave / WR;
 
-  unsigned char* group = smem + wk * C::NB * C::STAGE;
+  const lds_bytes group = smem + wk * C::NB * C::STAGE;
 
   // ---- this workgroup's work
   int64_t u = 0, u_end = 1, before = 0;
   int s, h = 0, m = 0;
   if constexpr (STREAM) {
     auto weight = [&](int i) { return seq_work<C>(p, i); };
-    const int64_t total = sum_all(p.S, lane, weight);
+    const int64_t total = sum_all(p.S, lane0, weight);
     const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
     u = blockIdx.x * per, u_end = min(total, u + per);
     if (u >= u_end) return;
-    s = find(p.S, lane, u, weight, before);
+    s = find(p.S, lane0, u, weight, before);
   } else {
     auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at<const int32_t*>(p, i)); };
     // the last tiles, which see the most keys, first
     const int64_t tiles = gridDim.x / p.Hkv;
     h = blockIdx.x % p.Hkv;
-    s = find(p.S, lane, tiles - 1 - blockIdx.x / p.Hkv, weight, before);
+    s = find(p.S, lane0, tiles - 1 - blockIdx.x / p.Hkv, weight, before);
     if (s >= p.S) return;
     m = (int)(tiles - 1 - blockIdx.x / p.Hkv - before);
   }
@@ -219,7 +233,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       h = (int)(item / tiles), m = (int)(item - (int64_t)h * tiles);
     }
     const bool whole = unit_lo == 0 && unit_hi == units;
-    // ---- rows
+    // ---- rows (what lanes derive from their number is not kept over the items: it would take some 40 registers)
+    const int lane = anew(lane0), hh = lane >> 5, ql = lane & 31, gt = wr * 64 + lane;
     const int n_rows = q.n * p.G, r0 = m * C::R, wrow = r0 + wr * 32;
     const int pos0 = q.len - q.n;  // of token 0
     const int i_first = r0 / p.G, i_last = (min(r0 + C::R, n_rows) - 1) / p.G;
@@ -236,11 +251,13 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 
     bf16x8 qf[C::NQ];
     {
-      const uint16_t* qp = p.q + (q.q0 + tok) * p.q_ld + (int64_t)head * D + 8 * hh;
+      // a K load of 16 codes is two steps' operand
+      constexpr bool PAIRS = C::KREG && C::QUANT;
+      const uint16_t* qp = p.q + (q.q0 + tok) * p.q_ld + (int64_t)head * D + (PAIRS ? 16 : 8) * hh;
 #pragma unroll
       for (int i = 0; i < C::NQ; ++i) {
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (live) v = *reinterpret_cast<const u32x4*>(qp + 16 * i);
+        if (live) v = *reinterpret_cast<const u32x4*>(qp + (PAIRS ? 32 * (i / 2) + 8 * (i % 2) : 16 * i));
         qf[i] = __builtin_bit_cast(bf16x8, v);
       }
     }
@@ -258,7 +275,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     float rs[C::NS];
     unsigned bad = 0;   // bit i: page i is none
     int page[C::NP];    // of the next tile: a scalar load's latency ahead
-    // The 64 lanes of a load read rows of one page: they begin at a multiple of, and are at most, 16.  lookup(i): which
+    // The 64 lanes of a load of whole rows read rows of one page: they begin at a multiple of, and are at most, 16.  lookup(i): which
     // of the wave's page numbers load i takes; first_row(i): its first row.
     auto lookup = [&](int i) { return WR == 1 ? i * 64 / C::CPR / 16 : i; };
     auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
@@ -267,93 +284,139 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
       for (int i = 0; i < C::NP; ++i) page[i] = page_of(k0 + (WR == 1 ? 16 * i : first_row(i)));
     };
-    auto issue = [&](int j) {
+    int64_t prow[C::NP];  // first cached row of the page's part of the tile
+    auto find_rows = [&](int j) {
       const int k0 = key_of(j);
       bad = 0;
-      int64_t row[C::NP];  // first row of the page's part
 #pragma unroll
       for (int i = 0; i < C::NP; ++i) {
         int n = page[i];
         if ((unsigned)n >= (unsigned)p.n_pages) n = 0, bad |= 1u << i;
-        row[i] = ((int64_t)n * p.Hkv + h) << p.page_shift;
+        prow[i] = (((int64_t)n * p.Hkv + h) << p.page_shift) + ((k0 + (WR == 1 ? 16 * i : first_row(i))) & page_mask);
       }
+      if (j + 1 < nt) look_up(j + 1);
+    };
+    auto issue_scales = [&](int j) {
+      const int k0 = key_of(j);
+#pragma unroll
+      for (int i = 0; i < C::NS; ++i) {
+        const int x = i * C::GT + gt, key = k0 + x % KT;
+        rs[i] = 0.0f;
+        if (x < 2 * KT && key >= kb && key < ke) {
+          const int n = p.pages[(int64_t)s * p.max_pages + (key >> p.page_shift)];
+          if ((unsigned)n < (unsigned)p.n_pages)
+            rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)n * p.Hkv + h) << p.page_shift) + (key & page_mask)];
+        }
+      }
+    };
+    // rows as they lie, 64 chunks a load
+    auto issue_rows = [&](const void* cache, u32x4* to) {
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        const int64_t at = (row[lookup(i)] + ((k0 + first_row(i)) & page_mask)) * C::ROWB;
-        rk[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k_cache) + at + lane * 16);
-        rv[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.v_cache) + at + lane * 16);
+        const int within = WR == 1 ? (first_row(i) & 15) : 0;
+        to[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(cache) +
+                                                (prow[lookup(i)] + within) * C::ROWB + lane * 16);
       }
-      if constexpr (C::QUANT) {
+    };
+    // as the instruction takes K: lane l its key 32 b + (l & 31), chunk 2 i + (l >> 5)
+    auto issue_k = [&]() {
 #pragma unroll
-        for (int i = 0; i < C::NS; ++i) {
-          const int x = i * C::GT + gt, key = k0 + x % KT;
-          rs[i] = 0.0f;
-          if (x < 2 * KT && key >= kb && key < ke) {
-            const int n = p.pages[(int64_t)s * p.max_pages + (key >> p.page_shift)];
-            if ((unsigned)n < (unsigned)p.n_pages)
-              rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)n * p.Hkv + h) << p.page_shift) + (key & page_mask)];
-          }
-        }
+      for (int b = 0; b < C::KB; ++b) {
+        const char* at = static_cast<const char*>(p.k_cache) +
+                         ((ql < 16 ? prow[C::KREG ? 2 * b : 0] : prow[C::KREG ? 2 * b + 1 : 0]) + (ql & 15)) * C::ROWB + 16 * hh;
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) rk[b * (C::CPR / 2) + i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
       }
-      if (j + 1 < nt) look_up(j + 1);
     };
     // this lane's place of load i
     const int c_lane = (wr * 64 + lane) % C::CPR, r_lane = (wr * 64 + lane) / C::CPR;
     auto store = [&](int j, int buf) {
       const int k0 = key_of(j);
-      unsigned char* lk = group + buf * C::STAGE;
-      unsigned char* lv = lk + KT * C::KROW;
+      const lds_bytes lk = group + buf * C::STAGE, lv = lk + C::KTILE;
+      const lds_bytes ak = lk + r_lane * C::KROW + c_lane * (C::QUANT ? 32 : 16);
+      const lds_bytes av = lv + r_lane * C::VROW + c_lane * (C::QUANT ? 32 : 16);
       const bool edge = k0 < kb || k0 + KT > ke;
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        const int r = r_lane + i * (C::GT / C::CPR);
+        constexpr int STEP = C::GT / C::CPR;  // rows from load to load
+        const int r = r_lane + i * STEP;
         const bool none = edge && (k0 + r < kb || k0 + r >= ke);
-        const bool no_page = (bad >> lookup(i) & 1) && !none;  // NaN scores for the rows that see it
+        const bool no_page = (bad >> lookup(i) & 1) && !none;
         const u32x4 zero = {0u, 0u, 0u, 0u}, nan = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-        if (none) rk[i] = zero;
         if (none || no_page) rv[i] = zero;
-        u32x4* tk = reinterpret_cast<u32x4*>(lk + r * C::KROW + c_lane * (C::QUANT ? 32 : 16));
-        u32x4* tv = reinterpret_cast<u32x4*>(lv + r * C::VROW + c_lane * (C::QUANT ? 32 : 16));
+        MOE_LDS u32x4* tk = lds_as<u32x4>(ak + i * STEP * C::KROW);
+        MOE_LDS u32x4* tv = lds_as<u32x4>(av + i * STEP * C::VROW);
+        u32x4 lo, hi;
+        if constexpr (!C::KREG) {
+          if (none) rk[i] = zero;
+          if constexpr (C::QUANT)
+            widen<C::CT>(rk[i], lo, hi);
+          else
+            lo = rk[i];
+          if (no_page) lo = hi = nan;  // NaN scores for the rows that see it
+          tk[0] = lo;
+          if constexpr (C::QUANT) tk[1] = hi;
+        }
         if constexpr (C::QUANT) {
-          u32x4 lo, hi;
-          widen<C::CT>(rk[i], lo, hi);
-          if (no_page) lo = hi = nan;
-          tk[0] = lo, tk[1] = hi;
           widen<C::CT>(rv[i], lo, hi);
           tv[0] = lo, tv[1] = hi;
         } else {
-          tk[0] = no_page ? nan : rk[i];
           tv[0] = rv[i];
         }
       }
-      if constexpr (C::QUANT) {
-        float* ls = reinterpret_cast<float*>(lv + KT * C::VROW);
+    };
+    auto store_scales = [&](int buf) {
+      MOE_LDS float* ls = lds_as<float>(group + buf * C::STAGE + C::KTILE + KT * C::VROW);
 #pragma unroll
-        for (int i = 0; i < C::NS; ++i) {
-          const int x = i * C::GT + gt;
-          if (x < 2 * KT) ls[x] = x < KT ? rs[i] * p.scale : rs[i];
-        }
+      for (int i = 0; i < C::NS; ++i) {
+        const int x = i * C::GT + gt;
+        if (x < 2 * KT) ls[x] = x < KT ? rs[i] * p.scale : rs[i];
       }
     };
 
     f32x16 o[C::DB] = {};
     float mx = kNegInf, l = 0.0f;
-    auto compute = [&](int j, int buf) {
-      const int k0 = key_of(j);
-      if (!wave_live || k0 > w_hi || k0 >= ke || (p.window > 0 && k0 + KT - 1 <= w_lo - p.window)) return;
-      const unsigned char* lk = group + buf * C::STAGE + ql * C::KROW + hh * 16;
-      const unsigned char* lv = group + buf * C::STAGE + KT * C::KROW;
-      const float* ls = reinterpret_cast<const float*>(lv + KT * C::VROW);
-      f32x16 x[C::KB] = {};
+    // whether this wave's rows see any key of the tile
+    auto any_seen = [&](int k0) {
+      return wave_live && k0 <= w_hi && k0 < ke && !(p.window > 0 && k0 + KT - 1 <= w_lo - p.window);
+    };
+    auto scores = [&](int buf, f32x16* x) {
+      const lds_bytes lk = group + buf * C::STAGE + ql * C::KROW + hh * 16;
 #pragma unroll
       for (int i = 0; i < C::NQ; ++i)
 #pragma unroll
         for (int b = 0; b < C::KB; ++b)
-          x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8*>(lk + 32 * b * C::KROW + 32 * i), qf[i], x[b], 0, 0, 0);
-      // ---- softmax
+          x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*lds_as<bf16x8>(lk + 32 * b * C::KROW + 32 * i), qf[i], x[b],
+                                                         0, 0, 0);
+    };
+    auto scores_k = [&](f32x16* x) {
+#pragma unroll
+      for (int b = 0; b < C::KB; ++b) {
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) {
+          const u32x4 k = rk[b * (C::CPR / 2) + i];
+          if constexpr (C::QUANT) {
+            u32x4 lo, hi;
+            widen<C::CT>(k, lo, hi);
+            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, lo), qf[2 * i], x[b], 0, 0, 0);
+            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi), qf[2 * i + 1], x[b], 0, 0, 0);
+          } else {
+            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k), qf[i], x[b], 0, 0, 0);
+          }
+        }
+        if (bad >> 2 * b & 3) {  // keys 32 b .. + 15 or + 16 .. + 31 have no page
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (bad >> (2 * b + (e >> 3)) & 1) x[b][e] = __builtin_nanf("");
+        }
+      }
+    };
+    // scores to weights
+    auto softmax = [&](int k0, int buf, f32x16* x) {
+      const MOE_LDS f32x4* ls =
+          lds_as<f32x4>(group + buf * C::STAGE + C::KTILE + KT * C::VROW + 16 * hh);
       const bool masked = k0 + KT - 1 > w_lo || (p.window > 0 && k0 <= w_hi - p.window);
 #pragma unroll
       for (int b = 0; b < C::KB; ++b)
@@ -361,8 +424,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         for (int g = 0; g < 4; ++g) {
           float f[4] = {p.scale, p.scale, p.scale, p.scale};
           if constexpr (C::QUANT) {
-            const float4 t = *reinterpret_cast<const float4*>(ls + 32 * b + 8 * g + 4 * hh);
-            f[0] = t.x, f[1] = t.y, f[2] = t.z, f[3] = t.w;
+            const f32x4 t = ls[8 * b + 2 * g];
+            f[0] = t[0], f[1] = t[1], f[2] = t[2], f[3] = t[3];
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= f[i];
@@ -403,13 +466,17 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         for (int b = 0; b < C::KB; ++b)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const float4 t = *reinterpret_cast<const float4*>(ls + KT + 32 * b + 8 * g + 4 * hh);
-            x[b][4 * g] *= t.x, x[b][4 * g + 1] *= t.y, x[b][4 * g + 2] *= t.z, x[b][4 * g + 3] *= t.w;
+            const f32x4 t = ls[KT / 4 + 8 * b + 2 * g];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= t[i];
           }
       }
-      // ---- O += P V
+    };
+    // O += P V
+    auto product = [&](int buf, const f32x16* x) {
+      const lds_bytes lv = group + buf * C::STAGE + C::KTILE;
       // lane j of 16 reads row j / 4, elements 4 (j % 4) .. + 3, and gets element j of the four rows
-      const unsigned char* tv = lv + (4 * hh + (lane >> 2 & 3)) * C::VROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+      const lds_bytes tv = lv + (4 * hh + (lane >> 2 & 3)) * C::VROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
@@ -425,10 +492,9 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           const bf16x8 pf = __builtin_bit_cast(bf16x8, pk);
 #pragma unroll
           for (int d = 0; d < C::DB; ++d) {
-            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const unsigned char* at = tv + (32 * b + 16 * t) * C::VROW + 64 * d;
-            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
-            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 8 * C::VROW));
+            const lds_bytes at = tv + (32 * b + 16 * t) * C::VROW + 64 * d;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_as<s16x4>(at));
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_as<s16x4>(at + 8 * C::VROW));
             const auto v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pf, o[d], 0, 0, 0);
             if constexpr (C::TERMS == 2)
@@ -444,16 +510,61 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       else
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
-    if (nt > 0) {
+    if constexpr (C::KREG) {
+      // a wave alone: K of the next tile is in flight from the end of the scores on, V from the end of its store on
+      if (nt > 0) {
+        look_up(0);
+        find_rows(0);
+        issue_k();
+        if constexpr (C::QUANT) issue_scales(0);
+        issue_rows(p.v_cache, rv);
+      }
+      for (int j = 0; j < nt; ++j) {
+        const int k0 = key_of(j);
+        const bool seen = any_seen(k0);
+        f32x16 x[C::KB] = {};
+        scores_k(x);
+        sync();  // the last tile's reads are done
+        if constexpr (C::QUANT) store_scales(0);
+        store(j, 0);
+        if (j + 1 < nt) {
+          find_rows(j + 1);
+          issue_k();
+          if constexpr (C::QUANT) issue_scales(j + 1);
+          issue_rows(p.v_cache, rv);
+        }
+        sync();
+        if (seen) {
+          softmax(k0, 0, x);
+          product(0, x);
+        }
+      }
+      sync();
+    } else if (nt > 0) {
+      auto issue = [&](int j) {
+        find_rows(j);
+        issue_rows(p.k_cache, rk);
+        issue_rows(p.v_cache, rv);
+        if constexpr (C::QUANT) issue_scales(j);
+      };
       look_up(0);
       issue(0);
       store(0, 0);
+      if constexpr (C::QUANT) store_scales(0);
       if (nt > 1) issue(1);
       sync();
       for (int j = 0; j < nt; ++j) {
-        compute(j, C::NB == 2 ? j & 1 : 0);
-        if constexpr (C::NB == 1) sync();
-        if (j + 1 < nt) store(j + 1, C::NB == 2 ? (j + 1) & 1 : 0);
+        const int k0 = key_of(j), buf = j & 1;
+        if (any_seen(k0)) {
+          f32x16 x[C::KB] = {};
+          scores(buf, x);
+          softmax(k0, buf, x);
+          product(buf, x);
+        }
+        if (j + 1 < nt) {
+          store(j + 1, buf ^ 1);
+          if constexpr (C::QUANT) store_scales(buf ^ 1);
+        }
         if (j + 2 < nt) issue(j + 2);
         sync();
       }
@@ -545,24 +656,25 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       if (WR > 1 && STREAM) __syncthreads();  // the next item's first tile
     } else {
       // the waves' results of the same rows joined: each adds its share of the elements of all
-      float2* ml = reinterpret_cast<float2*>(smem + WK * C::NB * C::STAGE);  // [WK][32]
-      float* mine = reinterpret_cast<float*>(group);                        // [16 DB][64]
-      if (hh == 0) ml[wk * 32 + ql] = make_float2(mx, l);
+      MOE_LDS f32x2* ml = lds_as<f32x2>(smem + WK * C::NB * C::STAGE) + anew(ql);  // [WK][32]
+      MOE_LDS float* mine = lds_as<float>(group) + anew(lane);                    // [16 DB][64]
+      if (hh == 0) ml[wk * 32] = f32x2{mx, l};
       __syncthreads();
       float all = kNegInf, sum = 0.0f;
-      float2 part[WK];
+      f32x2 part[WK];
 #pragma unroll
-      for (int w = 0; w < WK; ++w) part[w] = ml[w * 32 + ql], all = fmaxf(all, part[w].x);
+      for (int w = 0; w < WK; ++w) part[w] = ml[w * 32], all = fmaxf(all, part[w][0]);
       const float sub = all == kNegInf ? 0.0f : all;
 #pragma unroll
-      for (int w = 0; w < WK; ++w) sum += part[w].y * exp2_fast(part[w].x - sub);
+      for (int w = 0; w < WK; ++w) sum += part[w][1] * exp2_fast(part[w][0] - sub);
       const float f = exp2_fast(mx - sub);
 #pragma unroll
       for (int d = 0; d < C::DB; ++d)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64 + lane] = o[d][e] * f;
+        for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = o[d][e] * f;
       __syncthreads();
       const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const int lane_at = anew(lane);
       constexpr int PER = C::DB * 4 / WK;  // groups of four registers a wave adds up
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -572,7 +684,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         for (int w = 0; w < WK; ++w)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] += reinterpret_cast<const float*>(smem + w * C::NB * C::STAGE)[(4 * g4 + e) * 64 + lane];
+            v[e] += lds_as<float>(smem + w * C::NB * C::STAGE)[(4 * g4 + e) * 64 + lane_at];
         put4(32 * (g4 >> 2) + 8 * (g4 & 3) + 4 * hh, v, inv);
       }
       if (wk == 0) put_sums(all, sum);
@@ -585,7 +697,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 template <class C, bool STREAM>
 __global__ __launch_bounds__(C::THREADS, C::D == 256 ? 1 : 2) void attention_kernel(AttentionArgs p, int min_units) {
   extern __shared__ __align__(16) unsigned char smem[];
-  attention_body<C, STREAM>(p, min_units, smem);
+  attention_body<C, STREAM>(p, min_units, (lds_bytes)smem);
 }
 
 // ---- host
