@@ -64,7 +64,7 @@ struct Cfg {
   static constexpr bool KREG = WR == 1;  // K goes from memory into the operand registers
   static constexpr int KTILE = KREG ? 0 : KT * KROW;
   static constexpr int STAGE = (KTILE + KT * VROW > 32 * D * 4 || WK == 1 ? KTILE + KT * VROW : 32 * D * 4) + SCALES;
-  static constexpr int NP = WR == 1 ? KT / 16 : NL;  // page numbers a wave looks up per tile
+  static constexpr int NP = KT / 16;  // keys that share a page, whatever its size
   static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
@@ -121,6 +121,7 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
 // Sum of weight(s) over all sequences.
 template <class W>
 __device__ __forceinline__ int64_t sum_all(int S, int lane, W weight) {
+  if (S == 1) return lane_value(weight(0), 0);
   int64_t sum = 0;
   for (int b = 0; b < S; b += 64) sum += b + lane < S ? weight(b + lane) : 0;
   return lane_value(wave_scan(sum, lane), 63);
@@ -129,6 +130,7 @@ __device__ __forceinline__ int64_t sum_all(int S, int lane, W weight) {
 template <class W>
 __device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64_t& before) {
   before = 0;
+  if (S == 1) return at < lane_value(weight(0), 0) ? 0 : 1;
   for (int b = 0; b < S; b += 64) {
     const int64_t incl = before + wave_scan(b + lane < S ? weight(b + lane) : 0, lane);
     const int n = __popcll(__ballot(incl <= at));
@@ -273,50 +275,49 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 
     u32x4 rk[C::NL], rv[C::NL];
     float rs[C::NS];
-    unsigned bad = 0;   // bit i: page i is none
-    int page[C::NP];    // of the next tile: a scalar load's latency ahead
-    // The 64 lanes of a load of whole rows read rows of one page: they begin at a multiple of, and are at most, 16.  lookup(i): which
-    // of the wave's page numbers load i takes; first_row(i): its first row.
-    auto lookup = [&](int i) { return WR == 1 ? i * 64 / C::CPR / 16 : i; };
-    auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
+    unsigned bad = 0;     // bit g: keys 16 g .. + 15 of the tile have no page
+    int page[C::NP];      // of the next tile: a scalar load's latency ahead
+    int64_t prow[C::NP];  // first cached row of each 16 keys
     auto look_up = [&](int j) {
       const int k0 = key_of(j);
 #pragma unroll
-      for (int i = 0; i < C::NP; ++i) page[i] = page_of(k0 + (WR == 1 ? 16 * i : first_row(i)));
+      for (int g = 0; g < C::NP; ++g) page[g] = page_of(k0 + 16 * g);
     };
-    int64_t prow[C::NP];  // first cached row of the page's part of the tile
     auto find_rows = [&](int j) {
       const int k0 = key_of(j);
       bad = 0;
 #pragma unroll
-      for (int i = 0; i < C::NP; ++i) {
-        int n = page[i];
-        if ((unsigned)n >= (unsigned)p.n_pages) n = 0, bad |= 1u << i;
-        prow[i] = (((int64_t)n * p.Hkv + h) << p.page_shift) + ((k0 + (WR == 1 ? 16 * i : first_row(i))) & page_mask);
+      for (int g = 0; g < C::NP; ++g) {
+        int n = page[g];
+        if ((unsigned)n >= (unsigned)p.n_pages) n = 0, bad |= 1u << g;
+        prow[g] = (((int64_t)n * p.Hkv + h) << p.page_shift) + ((k0 + 16 * g) & page_mask);
       }
       if (j + 1 < nt) look_up(j + 1);
+    };
+    auto row_of = [&](int g) {
+      int64_t r = prow[0];
+#pragma unroll
+      for (int i = 1; i < C::NP; ++i) r = g == i ? prow[i] : r;
+      return r;
     };
     auto issue_scales = [&](int j) {
       const int k0 = key_of(j);
 #pragma unroll
       for (int i = 0; i < C::NS; ++i) {
-        const int x = i * C::GT + gt, key = k0 + x % KT;
+        const int x = i * C::GT + gt, kk = x % KT, key = k0 + kk;
         rs[i] = 0.0f;
-        if (x < 2 * KT && key >= kb && key < ke) {
-          const int n = p.pages[(int64_t)s * p.max_pages + (key >> p.page_shift)];
-          if ((unsigned)n < (unsigned)p.n_pages)
-            rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)n * p.Hkv + h) << p.page_shift) + (key & page_mask)];
-        }
+        if (x < 2 * KT && key >= kb && key < ke && !(bad >> (kk >> 4) & 1))
+          rs[i] = (x < KT ? p.k_scale : p.v_scale)[row_of(kk >> 4) + (kk & 15)];
       }
     };
-    // rows as they lie, 64 chunks a load
+    // rows as they lie, 64 chunks a load: these begin at a multiple of, and are at most, 16 rows
+    auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
     auto issue_rows = [&](const void* cache, u32x4* to) {
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        const int within = WR == 1 ? (first_row(i) & 15) : 0;
         to[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(cache) +
-                                                (prow[lookup(i)] + within) * C::ROWB + lane * 16);
+                                                (row_of(first_row(i) >> 4) + (first_row(i) & 15)) * C::ROWB + lane * 16);
       }
     };
     // as the instruction takes K: lane l its key 32 b + (l & 31), chunk 2 i + (l >> 5)
@@ -324,7 +325,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
       for (int b = 0; b < C::KB; ++b) {
         const char* at = static_cast<const char*>(p.k_cache) +
-                         ((ql < 16 ? prow[C::KREG ? 2 * b : 0] : prow[C::KREG ? 2 * b + 1 : 0]) + (ql & 15)) * C::ROWB + 16 * hh;
+                         ((ql < 16 ? prow[2 * b] : prow[2 * b + 1]) + (ql & 15)) * C::ROWB + 16 * hh;
 #pragma unroll
         for (int i = 0; i < C::CPR / 2; ++i) rk[b * (C::CPR / 2) + i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
       }
@@ -343,7 +344,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         constexpr int STEP = C::GT / C::CPR;  // rows from load to load
         const int r = r_lane + i * STEP;
         const bool none = edge && (k0 + r < kb || k0 + r >= ke);
-        const bool no_page = (bad >> lookup(i) & 1) && !none;
+        const bool no_page = (bad >> (first_row(i) >> 4) & 1) && !none;
         const u32x4 zero = {0u, 0u, 0u, 0u}, nan = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
         if (none || no_page) rv[i] = zero;
         MOE_LDS u32x4* tk = lds_as<u32x4>(ak + i * STEP * C::KROW);
@@ -418,18 +419,17 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       const MOE_LDS f32x4* ls =
           lds_as<f32x4>(group + buf * C::STAGE + C::KTILE + KT * C::VROW + 16 * hh);
       const bool masked = k0 + KT - 1 > w_lo || (p.window > 0 && k0 <= w_hi - p.window);
+      if constexpr (C::QUANT) {
 #pragma unroll
-      for (int b = 0; b < C::KB; ++b)
+        for (int b = 0; b < C::KB; ++b)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float f[4] = {p.scale, p.scale, p.scale, p.scale};
-          if constexpr (C::QUANT) {
+          for (int g = 0; g < 4; ++g) {
             const f32x4 t = ls[8 * b + 2 * g];
-            f[0] = t[0], f[1] = t[1], f[2] = t[2], f[3] = t[3];
-          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= f[i];
-        }
+            for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= t[i];
+          }
+      }
+      const float scale = C::QUANT ? 1.0f : p.scale;  // 8-bit keys: in the scales
       if (masked) {
 #pragma unroll
         for (int b = 0; b < C::KB; ++b)
@@ -444,7 +444,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, x[b][e]);
-      top = halves_max(top);
+      top = halves_max(top) * scale;
       if (__any(top > mx + kSlack)) {
         const float to = fmaxf(mx, top);
         const float f = exp2_fast(mx - (to == kNegInf ? 0.0f : to));
@@ -458,7 +458,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          x[b][e] = exp2_fast(x[b][e] - sub);
+          x[b][e] = exp2_fast(fmaf(x[b][e], scale, -sub));
           l += x[b][e];
         }
       if constexpr (C::QUANT) {

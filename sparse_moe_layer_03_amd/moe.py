@@ -486,32 +486,56 @@ def _rows(name, t, n, width):
     """(pointer, elements from row to row) of n rows of `width` bf16 elements: a tensor whose rows are whole (the part
     of a wider matrix's columns, say) or one that _args takes for [n, width].  Raw pointers stand for rows without
     gaps."""
-    import torch
     if t is None or t.__class__ is int:
         return t, width
-    if (t.dtype is torch.bfloat16 and t.dim() > 1 and t.shape[0] >= n > 0 and math.prod(t.shape[1:]) == width
-            and t[0].is_contiguous()):
-        at = t.get_device()
-        if at < 0:
-            raise ValueError(f"{name} is on {t.device}, not on a GPU")
-        if at != _device():
-            raise ValueError(f"{name} is on GPU {at}; the current one is {_device()}")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
-    return _args((name, t, torch.bfloat16, (n, width)))[0], width
+    if t.dtype is _bf16():
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2:
+            whole = shape[1] == width and stride[1] == 1
+        else:
+            whole = len(shape) > 2 and math.prod(shape[1:]) == width and t[:1].is_contiguous()
+        if whole and shape[0] >= n > 0:
+            at = t.get_device()
+            if at == _device():
+                return t.data_ptr(), stride[0] if shape[0] > 1 else width
+            if at >= 0:
+                raise ValueError(f"{name} is on GPU {at}; the current one is {_device()}")
+    return _args((name, t, _bf16(), (n, width)))[0], width
+
+
+def _bf16():
+    global _bf16
+    import torch
+    bf = torch.bfloat16
+    _bf16 = lambda: bf  # noqa: E731
+    return bf
+
+
+def _cache_types():
+    """MOE_ type of a cache by its tensors' type."""
+    global _cache_types
+    import torch
+    types = {torch.bfloat16: BF16, torch.int8: I8, torch.float8_e4m3fn: E4M3}
+    _cache_types = lambda: types  # noqa: E731
+    return types
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D):
     """(MOE_ type, pointers) of a cache, whose type is its tensors'."""
     import torch
-    types = {torch.bfloat16: BF16, torch.int8: I8, torch.float8_e4m3fn: E4M3}
     if k_cache is None or k_cache.__class__ is int:
         raise ValueError("k_cache must be a tensor: its type is the call's")
-    if k_cache.dtype not in types:
-        raise ValueError(f"k_cache is {k_cache.dtype}; expected {', '.join(map(str, types))}")
+    dtype = k_cache.dtype
+    types = _cache_types()
+    if dtype not in types:
+        raise ValueError(f"k_cache is {dtype}; expected {', '.join(map(str, types))}")
     shape = (n_pages, Hkv, P, D)
-    return types[k_cache.dtype], _args(
-        ("k_cache", k_cache, k_cache.dtype, shape), ("v_cache", v_cache, k_cache.dtype, shape),
-        ("k_scale", k_scale, torch.float32, shape[:3]), ("v_scale", v_scale, torch.float32, shape[:3]))
+    if k_scale is None and v_scale is None:
+        return types[dtype], _args(("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape)) + [None, None]
+    scales = (n_pages, Hkv, P)
+    return types[dtype], _args(
+        ("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape),
+        ("k_scale", k_scale, torch.float32, scales), ("v_scale", v_scale, torch.float32, scales))
 
 
 def moe_rope_frequencies(rot: int, base: float, scaling: int = ROPE_PLAIN, factor: float = 1.0,
