@@ -157,7 +157,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // Sixteen codes as two chunks of bf16 (every code is one exactly).
 template <int CT>
-__device__ __forceinline__ void widen(const u32x4& w, u32x4& lo, u32x4& hi) {
+__device__ __forceinline__ void widen(u32x4 w, u32x4& lo, u32x4& hi) {
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -277,99 +277,111 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     float rs[C::NS];
     unsigned bad = 0;     // bit g: keys 16 g .. + 15 of the tile have no page
     int page[C::NP];      // of the next tile: a scalar load's latency ahead
-    int64_t prow[C::NP];  // first cached row of each 16 keys
+    int at_page[C::NP];   // of the tile at hand; page 0 stands for none
     auto look_up = [&](int j) {
       const int k0 = key_of(j);
+      page[0] = page_of(k0);
+      // (tiles begin at multiples of their size)
+      if (KT >> p.page_shift > 1) {
 #pragma unroll
-      for (int g = 0; g < C::NP; ++g) page[g] = page_of(k0 + 16 * g);
+        for (int g = 1; g < C::NP; ++g) page[g] = page_of(k0 + 16 * g);
+      } else {
+#pragma unroll
+        for (int g = 1; g < C::NP; ++g) page[g] = page[0];
+      }
     };
-    auto find_rows = [&](int j) {
-      const int k0 = key_of(j);
+    auto find_pages = [&](int j) {
       bad = 0;
 #pragma unroll
       for (int g = 0; g < C::NP; ++g) {
-        int n = page[g];
-        if ((unsigned)n >= (unsigned)p.n_pages) n = 0, bad |= 1u << g;
-        prow[g] = (((int64_t)n * p.Hkv + h) << p.page_shift) + ((k0 + 16 * g) & page_mask);
+        at_page[g] = page[g];
+        if ((unsigned)page[g] >= (unsigned)p.n_pages) at_page[g] = 0, bad |= 1u << g;
       }
       if (j + 1 < nt) look_up(j + 1);
     };
-    auto row_of = [&](int g) {
-      int64_t r = prow[0];
+    // first cached row of a tile's keys 16 g .. (a selection of array elements by a lane's g would put them into memory)
+    auto row_of = [&](const int* at, int j, int g) {
+      int n = at[0];
 #pragma unroll
-      for (int i = 1; i < C::NP; ++i) r = g == i ? prow[i] : r;
-      return r;
+      for (int i = 1; i < C::NP; ++i) n += g >= i ? at[i] - at[i - 1] : 0;
+      return (((int64_t)n * p.Hkv + h) << p.page_shift) + ((key_of(j) + 16 * g) & page_mask);
     };
-    auto issue_scales = [&](int j) {
+    auto issue_scales = [&](int j, const int* at, unsigned none) {
       const int k0 = key_of(j);
 #pragma unroll
       for (int i = 0; i < C::NS; ++i) {
         const int x = i * C::GT + gt, kk = x % KT, key = k0 + kk;
         rs[i] = 0.0f;
-        if (x < 2 * KT && key >= kb && key < ke && !(bad >> (kk >> 4) & 1))
-          rs[i] = (x < KT ? p.k_scale : p.v_scale)[row_of(kk >> 4) + (kk & 15)];
+        if (x < 2 * KT && key >= kb && key < ke && !(none >> (kk >> 4) & 1))
+          rs[i] = (x < KT ? p.k_scale : p.v_scale)[row_of(at, j, kk >> 4) + (kk & 15)];
       }
     };
     // rows as they lie, 64 chunks a load: these begin at a multiple of, and are at most, 16 rows
     auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
-    auto issue_rows = [&](const void* cache, u32x4* to) {
+    auto issue_rows = [&](const void* cache, u32x4* to, int j, const int* at) {
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        to[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(cache) +
-                                                (row_of(first_row(i) >> 4) + (first_row(i) & 15)) * C::ROWB + lane * 16);
+        const int64_t row = row_of(at, j, first_row(i) >> 4) + (first_row(i) & 15);
+        to[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(cache) + row * C::ROWB + lane * 16);
       }
     };
     // as the instruction takes K: lane l its key 32 b + (l & 31), chunk 2 i + (l >> 5)
-    auto issue_k = [&]() {
+    auto issue_k = [&](int j) {
 #pragma unroll
       for (int b = 0; b < C::KB; ++b) {
         const char* at = static_cast<const char*>(p.k_cache) +
-                         ((ql < 16 ? prow[2 * b] : prow[2 * b + 1]) + (ql & 15)) * C::ROWB + 16 * hh;
+                         (row_of(at_page, j, 2 * b + (ql >> 4)) + (ql & 15)) * C::ROWB + 16 * hh;
 #pragma unroll
         for (int i = 0; i < C::CPR / 2; ++i) rk[b * (C::CPR / 2) + i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
       }
     };
     // this lane's place of load i
     const int c_lane = (wr * 64 + lane) % C::CPR, r_lane = (wr * 64 + lane) / C::CPR;
-    auto store = [&](int j, int buf) {
+    // to LDS as bf16.  Rows outside the tile's range of keys become zeros; without a page (none: its bits) K becomes NaN,
+    // and with it the scores of the rows that see it, V zeros.
+    auto store_rows = [&](u32x4* from, int j, lds_bytes to, int row_bytes, unsigned none, bool is_k) {
       const int k0 = key_of(j);
-      const lds_bytes lk = group + buf * C::STAGE, lv = lk + C::KTILE;
-      const lds_bytes ak = lk + r_lane * C::KROW + c_lane * (C::QUANT ? 32 : 16);
-      const lds_bytes av = lv + r_lane * C::VROW + c_lane * (C::QUANT ? 32 : 16);
+      const lds_bytes at = to + r_lane * row_bytes + c_lane * (C::QUANT ? 32 : 16);
       const bool edge = k0 < kb || k0 + KT > ke;
+      constexpr int STEP = C::GT / C::CPR;  // rows from load to load
+      if (edge || none) {
+#pragma unroll
+        for (int i = 0; i < C::NL; ++i) {
+          const int key = k0 + r_lane + i * STEP;
+          const bool out = key < kb || key >= ke, no_page = (none >> (first_row(i) >> 4) & 1) && !out;
+          // codes have no NaN in all types: theirs is put in below
+          const uint32_t v = no_page && is_k && !C::QUANT ? 0x7fc07fc0u : 0u;
+          if (out || no_page) from[i] = u32x4{v, v, v, v};
+        }
+      }
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        constexpr int STEP = C::GT / C::CPR;  // rows from load to load
-        const int r = r_lane + i * STEP;
-        const bool none = edge && (k0 + r < kb || k0 + r >= ke);
-        const bool no_page = (bad >> (first_row(i) >> 4) & 1) && !none;
-        const u32x4 zero = {0u, 0u, 0u, 0u}, nan = {0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-        if (none || no_page) rv[i] = zero;
-        MOE_LDS u32x4* tk = lds_as<u32x4>(ak + i * STEP * C::KROW);
-        MOE_LDS u32x4* tv = lds_as<u32x4>(av + i * STEP * C::VROW);
-        u32x4 lo, hi;
-        if constexpr (!C::KREG) {
-          if (none) rk[i] = zero;
-          if constexpr (C::QUANT)
-            widen<C::CT>(rk[i], lo, hi);
-          else
-            lo = rk[i];
-          if (no_page) lo = hi = nan;  // NaN scores for the rows that see it
-          tk[0] = lo;
-          if constexpr (C::QUANT) tk[1] = hi;
-        }
+        MOE_LDS u32x4* t = lds_as<u32x4>(at + i * STEP * row_bytes);
         if constexpr (C::QUANT) {
-          widen<C::CT>(rv[i], lo, hi);
-          tv[0] = lo, tv[1] = hi;
+          u32x4 lo, hi;
+          widen<C::CT>(from[i], lo, hi);
+          t[0] = lo, t[1] = hi;
         } else {
-          tv[0] = rv[i];
+          t[0] = from[i];
+        }
+      }
+      if (C::QUANT && is_k && none) {
+#pragma unroll
+        for (int i = 0; i < C::NL; ++i) {
+          const int key = k0 + r_lane + i * STEP;
+          if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
+          if ((none >> (first_row(i) >> 4) & 1) && key >= kb && key < ke)
+            lds_as<u32x4>(at + i * STEP * row_bytes)[0] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
         }
       }
     };
+    auto buf_v = [&](int buf) { return group + buf * C::STAGE + C::KTILE; };
+    auto store_k = [&](int j, int buf, unsigned none) { store_rows(rk, j, group + buf * C::STAGE, C::KROW, none, true); };
+    auto store_v = [&](int j, int buf, unsigned none) { store_rows(rv, j, buf_v(buf), C::VROW, none, false); };
     auto store_scales = [&](int buf) {
-      MOE_LDS float* ls = lds_as<float>(group + buf * C::STAGE + C::KTILE + KT * C::VROW);
+      MOE_LDS float* ls = lds_as<float>(buf_v(buf) + KT * C::VROW);
 #pragma unroll
       for (int i = 0; i < C::NS; ++i) {
         const int x = i * C::GT + gt;
@@ -414,22 +426,21 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         }
       }
     };
-    // scores to weights
-    auto softmax = [&](int k0, int buf, f32x16* x) {
-      const MOE_LDS f32x4* ls =
-          lds_as<f32x4>(group + buf * C::STAGE + C::KTILE + KT * C::VROW + 16 * hh);
+    const float scale = C::QUANT ? 1.0f : p.scale;  // 8-bit keys: in the scales
+    auto scales_at = [&](int buf) { return lds_as<f32x4>(buf_v(buf) + KT * C::VROW + 16 * hh); };
+    // masks the scores and brings m up to them
+    auto maximum = [&](int k0, int buf, f32x16* x) {
       const bool masked = k0 + KT - 1 > w_lo || (p.window > 0 && k0 <= w_hi - p.window);
       if constexpr (C::QUANT) {
 #pragma unroll
         for (int b = 0; b < C::KB; ++b)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const f32x4 t = ls[8 * b + 2 * g];
+            const f32x4 t = scales_at(buf)[8 * b + 2 * g];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= t[i];
           }
       }
-      const float scale = C::QUANT ? 1.0f : p.scale;  // 8-bit keys: in the scales
       if (masked) {
 #pragma unroll
         for (int b = 0; b < C::KB; ++b)
@@ -453,43 +464,49 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
         for (int d = 0; d < C::DB; ++d) o[d] *= f;
       }
+    };
+    // scores to weights, as operands: hi[2 b + t], and what their rounding leaves in lo
+    auto weights = [&](int buf, f32x16* x, u32x4* hi, u32x4* lo) {
       const float sub = mx == kNegInf ? 0.0f : mx;
+      float sum[4] = {};
 #pragma unroll
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[b][e] = exp2_fast(fmaf(x[b][e], scale, -sub));
-          l += x[b][e];
-        }
-      if constexpr (C::QUANT) {
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int b = 0; b < C::KB; ++b)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x4 t = ls[KT / 4 + 8 * b + 2 * g];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= t[i];
+          for (int e = 8 * t; e < 8 * t + 8; ++e) {
+            x[b][e] = exp2_fast(fmaf(x[b][e], scale, -sub));
+            sum[e & 3] += x[b][e];
           }
-      }
+          if constexpr (C::QUANT) {
+#pragma unroll
+            for (int g = 2 * t; g < 2 * t + 2; ++g) {
+              const f32x4 f = scales_at(buf)[KT / 4 + 8 * b + 2 * g];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[b][4 * g + i] *= f[i];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p0 = x[b][8 * t + 2 * i], p1 = x[b][8 * t + 2 * i + 1];
+            const uint32_t w = cvt_bf16x2(p0, p1);
+            hi[2 * b + t][i] = w;
+            if constexpr (C::TERMS == 2)
+              lo[2 * b + t][i] = cvt_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
+          }
+        }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
     // O += P V
-    auto product = [&](int buf, const f32x16* x) {
-      const lds_bytes lv = group + buf * C::STAGE + C::KTILE;
+    auto product = [&](int buf, const u32x4* hi, const u32x4* lo) {
+      const lds_bytes lv = buf_v(buf);
       // lane j of 16 reads row j / 4, elements 4 (j % 4) .. + 3, and gets element j of the four rows
       const lds_bytes tv = lv + (4 * hh + (lane >> 2 & 3)) * C::VROW + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
       for (int b = 0; b < C::KB; ++b)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          u32x4 pk, pl;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p0 = x[b][8 * t + 2 * i], p1 = x[b][8 * t + 2 * i + 1];
-            pk[i] = cvt_bf16x2(p0, p1);
-            if constexpr (C::TERMS == 2)
-              pl[i] = cvt_bf16x2(p0 - __uint_as_float(pk[i] << 16), p1 - __uint_as_float(pk[i] & 0xffff0000u));
-          }
-          const bf16x8 pf = __builtin_bit_cast(bf16x8, pk);
+          const bf16x8 pf = __builtin_bit_cast(bf16x8, hi[2 * b + t]);
 #pragma unroll
           for (int d = 0; d < C::DB; ++d) {
             const lds_bytes at = tv + (32 * b + 16 * t) * C::VROW + 64 * d;
@@ -499,7 +516,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pf, o[d], 0, 0, 0);
             if constexpr (C::TERMS == 2)
               o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                             __builtin_bit_cast(bf16x8, pl), o[d], 0, 0, 0);
+                                                             __builtin_bit_cast(bf16x8, lo[2 * b + t]), o[d], 0, 0, 0);
           }
         }
     };
@@ -510,64 +527,90 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       else
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
+    u32x4 hi[2 * C::KB], lo[2 * C::KB];
     if constexpr (C::KREG) {
-      // a wave alone: K of the next tile is in flight from the end of the scores on, V from the end of its store on
+      // a wave alone: the next tile is in flight from the end of this one's store on
+      auto issue = [&](int j) {
+        find_pages(j);
+        issue_k(j);
+        if constexpr (C::QUANT) issue_scales(j, at_page, bad);
+        issue_rows(p.v_cache, rv, j, at_page);
+      };
       if (nt > 0) {
         look_up(0);
-        find_rows(0);
-        issue_k();
-        if constexpr (C::QUANT) issue_scales(0);
-        issue_rows(p.v_cache, rv);
+        issue(0);
       }
       for (int j = 0; j < nt; ++j) {
         const int k0 = key_of(j);
-        const bool seen = any_seen(k0);
         f32x16 x[C::KB] = {};
         scores_k(x);
         sync();  // the last tile's reads are done
         if constexpr (C::QUANT) store_scales(0);
-        store(j, 0);
-        if (j + 1 < nt) {
-          find_rows(j + 1);
-          issue_k();
-          if constexpr (C::QUANT) issue_scales(j + 1);
-          issue_rows(p.v_cache, rv);
-        }
+        store_v(j, 0, bad);
+        if (j + 1 < nt) issue(j + 1);
         sync();
-        if (seen) {
-          softmax(k0, 0, x);
-          product(0, x);
+        if (any_seen(k0)) {
+          maximum(k0, 0, x);
+          weights(0, x, hi, lo);
+          product(0, hi, lo);
         }
       }
       sync();
     } else if (nt > 0) {
-      auto issue = [&](int j) {
-        find_rows(j);
-        issue_rows(p.k_cache, rk);
-        issue_rows(p.v_cache, rv);
-        if constexpr (C::QUANT) issue_scales(j);
+      // Scores run a tile ahead, so that their products and the exponentials of the tile before lie side by side.  Step
+      // j: LDS holds K of tile j + 1 and V of tile j, K of j + 2 and V of j + 1 are in flight.
+      int v_page[C::NP];
+      unsigned vbad = 0;
+      auto next_k = [&](int j) {
+        find_pages(j);
+        issue_rows(p.k_cache, rk, j, at_page);
+      };
+      auto to_v = [&]() {  // V follows K by a tile
+#pragma unroll
+        for (int g = 0; g < C::NP; ++g) v_page[g] = at_page[g];
+        vbad = bad;
+      };
+      auto next_v = [&](int j) {
+        issue_rows(p.v_cache, rv, j, v_page);
+        if constexpr (C::QUANT) issue_scales(j, v_page, vbad);
       };
       look_up(0);
-      issue(0);
-      store(0, 0);
+      next_k(0), to_v(), next_v(0);
+      store_k(0, 0, bad), store_v(0, 0, vbad);
       if constexpr (C::QUANT) store_scales(0);
-      if (nt > 1) issue(1);
-      sync();
-      for (int j = 0; j < nt; ++j) {
-        const int k0 = key_of(j), buf = j & 1;
-        if (any_seen(k0)) {
-          f32x16 x[C::KB] = {};
-          scores(buf, x);
-          softmax(k0, buf, x);
-          product(buf, x);
-        }
-        if (j + 1 < nt) {
-          store(j + 1, buf ^ 1);
-          if constexpr (C::QUANT) store_scales(buf ^ 1);
-        }
-        if (j + 2 < nt) issue(j + 2);
-        sync();
+      if (nt > 1) {
+        next_k(1);
+        to_v(), next_v(1);
+        store_k(1, 1, bad);
+        if (nt > 2) next_k(2);
       }
+      sync();
+      f32x16 x[C::KB] = {};
+      if (wave_live) scores(0, x);
+      sync();
+      auto step = [&](int j, auto last) {
+        const int buf = j & 1;
+        if (wave_live) {
+          maximum(key_of(j), buf, x);
+          weights(buf, x, hi, lo);
+          if constexpr (!decltype(last)::value) {
+#pragma unroll
+            for (int b = 0; b < C::KB; ++b) x[b] = f32x16{};
+            scores(buf ^ 1, x);
+          }
+          product(buf, hi, lo);
+        }
+        if constexpr (!decltype(last)::value) {
+          if (j + 2 < nt) store_k(j + 2, buf, bad);
+          store_v(j + 1, buf ^ 1, vbad);
+          if constexpr (C::QUANT) store_scales(buf ^ 1);
+          if (j + 2 < nt) to_v(), next_v(j + 2);
+          if (j + 3 < nt) next_k(j + 3);
+          sync();
+        }
+      };
+      for (int j = 0; j < nt - 1; ++j) step(j, std::false_type());
+      step(nt - 1, std::true_type());
     }
     l = halves_sum(l);
 
@@ -653,7 +696,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           }
         put_sums(mx, l);
       }
-      if (WR > 1 && STREAM) __syncthreads();  // the next item's first tile
+      if (WR > 1 && STREAM) __syncthreads();  // before the next item's first tile
     } else {
       // the waves' results of the same rows joined: each adds its share of the elements of all
       MOE_LDS f32x2* ml = lds_as<f32x2>(smem + WK * C::NB * C::STAGE) + anew(ql);  // [WK][32]
