@@ -56,7 +56,8 @@ struct Cfg {
   static constexpr int CHUNKS = KT * CPR;
   static constexpr int NL = (CHUNKS + GT - 1) / GT;
   static constexpr int NS = QUANT ? (2 * KT + GT - 1) / GT : 1;  // scales a thread loads
-  static constexpr int NB = WR == 1 ? 1 : 2;   // tiles in LDS: a wave alone needs no second one
+  static constexpr bool TWO = WR == 8;          // two groups of four waves, half a step apart
+  static constexpr int NB = WR == 1 ? 1 : TWO ? 3 : 2;  // tiles in LDS: a wave alone needs no second one
   // Bytes from row to row in LDS, bf16.  A K read takes one 16-byte chunk of 32 rows: 16 rows in a row lie in different
   // banks.  A transposing V read takes four rows of 64 bytes, which do so likewise.
   static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 64;
@@ -64,7 +65,9 @@ struct Cfg {
   static constexpr bool KREG = WR == 1;  // K goes from memory into the operand registers
   static constexpr int KTILE = KREG ? 0 : KT * KROW;
   static constexpr int STAGE = (KTILE + KT * VROW > 32 * D * 4 || WK == 1 ? KTILE + KT * VROW : 32 * D * 4) + SCALES;
-  static constexpr int NP = KT / 16;  // keys that share a page, whatever its size
+  // Page numbers a wave looks up per tile: of every load of whole rows, or of every 16 keys.  The 64 lanes of such a load
+  // read rows that begin at a multiple of, and are at most, 16, so they lie in one page whatever its size.
+  static constexpr int NP = KREG ? KT / 16 : NL;
   static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
@@ -180,10 +183,18 @@ __device__ __forceinline__ float cached(const void* p, int64_t i) {
   return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p)[i], 0);
 }
 
-// Partial results in the workspace: per slot R rows of O (unscaled, fp32), then R pairs (m, l).
+// Partial results in the workspace: a Part per workgroup, then slots of R rows of O (unscaled, fp32) and R pairs (m, l).
+// Part w: the item that begins in workgroup w's share and ends behind it.
+struct Part {
+  int n;     // workgroups that hold a part of it, w the first; 0: there is no such item
+  int rows;  // of the item
+  int row0;  // its first, in the sequence's (token, head) rows
+  int q0, h;
+  int none[3];
+};
 template <class C>
 __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
-  return p.partial + (size_t)slot * C::R * (C::D + 2);
+  return p.partial + (size_t)gridDim.x * (sizeof(Part) / 4) + (size_t)slot * C::R * (C::D + 2);
 }
 
 // One workgroup computes one (sequence, key head, row tile), or (STREAM) its equal share of all units of work, which
@@ -192,20 +203,24 @@ __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
 template <class C, bool STREAM>
 __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, lds_bytes smem) {
   constexpr int D = C::D, KT = C::KT, WR = C::WR, WK = C::WK;
+  constexpr bool KREG = C::KREG;
   const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave % WR, wk = wave / WR;
 
   const lds_bytes group = smem + wk * C::NB * C::STAGE;
 
   // ---- this workgroup's work
-  int64_t u = 0, u_end = 1, before = 0;
+  int64_t u = 0, u_end = 1, before = 0, share = 1;
   int s, h = 0, m = 0;
   if constexpr (STREAM) {
     auto weight = [&](int i) { return seq_work<C>(p, i); };
     const int64_t total = sum_all(p.S, lane0, weight);
     const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
     u = blockIdx.x * per, u_end = min(total, u + per);
+    // (written again below where there is such an item)
+    if (threadIdx.x == 0) reinterpret_cast<Part*>(p.partial)[blockIdx.x].n = 0;
     if (u >= u_end) return;
+    share = per;
     s = find(p.S, lane0, u, weight, before);
   } else {
     auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at<const int32_t*>(p, i)); };
@@ -275,63 +290,75 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 
     u32x4 rk[C::NL], rv[C::NL];
     float rs[C::NS];
-    unsigned bad = 0;     // bit g: keys 16 g .. + 15 of the tile have no page
-    int page[C::NP];      // of the next tile: a scalar load's latency ahead
-    int at_page[C::NP];   // of the tile at hand; page 0 stands for none
+    auto first_row = [&](int i) { return KREG ? 16 * i : (i * C::GT + wr * 64) / C::CPR; };  // of page number i
+    unsigned bad = 0;    // bit i: there is no such page
+    int page[C::NP];     // of the next tile: a scalar load's latency ahead
+    int64_t off[C::NP];  // of the tile at hand: where its rows begin in the cache, in bytes
+    const uint32_t page_bytes = (uint32_t)p.Hkv * C::ROWB << p.page_shift, head_bytes = (uint32_t)h * C::ROWB << p.page_shift;
     auto look_up = [&](int j) {
       const int k0 = key_of(j);
-      page[0] = page_of(k0);
-      // (tiles begin at multiples of their size)
-      if (KT >> p.page_shift > 1) {
 #pragma unroll
-        for (int g = 1; g < C::NP; ++g) page[g] = page_of(k0 + 16 * g);
-      } else {
-#pragma unroll
-        for (int g = 1; g < C::NP; ++g) page[g] = page[0];
-      }
+      for (int i = 0; i < C::NP; ++i) page[i] = page_of(k0 + first_row(i));
     };
-    auto find_pages = [&](int j) {
+    auto find_rows = [&](int j) {
+      const int k0 = key_of(j);
       bad = 0;
 #pragma unroll
-      for (int g = 0; g < C::NP; ++g) {
-        at_page[g] = page[g];
-        if ((unsigned)page[g] >= (unsigned)p.n_pages) at_page[g] = 0, bad |= 1u << g;
+      for (int i = 0; i < C::NP; ++i) {
+        const bool none = (unsigned)page[i] >= (unsigned)p.n_pages;
+        bad |= none ? 1u << i : 0u;
+        off[i] = (int64_t)((uint64_t)(none ? 0u : (unsigned)page[i]) * page_bytes) +
+                 (head_bytes + (uint32_t)((k0 + first_row(i)) & page_mask) * C::ROWB);
       }
       if (j + 1 < nt) look_up(j + 1);
     };
-    // first cached row of a tile's keys 16 g .. (a selection of array elements by a lane's g would put them into memory)
-    auto row_of = [&](const int* at, int j, int g) {
-      int n = at[0];
+    // Scales: a wave alone has the pages of all keys at hand; where more share a tile each lane looks up its own, a tile
+    // ahead.
+    int s_page[C::NS];
+    auto scale_key = [&](int j, int i) { return key_of(j) + (i * C::GT + gt) % KT; };
+    auto look_up_scales = [&](int j) {
+      if constexpr (KREG) return;
 #pragma unroll
-      for (int i = 1; i < C::NP; ++i) n += g >= i ? at[i] - at[i - 1] : 0;
-      return (((int64_t)n * p.Hkv + h) << p.page_shift) + ((key_of(j) + 16 * g) & page_mask);
+      for (int i = 0; i < C::NS; ++i)
+        s_page[i] = p.pages[(int64_t)s * p.max_pages + (min(max(scale_key(j, i), kb), ke - 1) >> p.page_shift)];
     };
-    auto issue_scales = [&](int j, const int* at, unsigned none) {
-      const int k0 = key_of(j);
+    auto issue_scales = [&](int j) {
 #pragma unroll
       for (int i = 0; i < C::NS; ++i) {
-        const int x = i * C::GT + gt, kk = x % KT, key = k0 + kk;
+        const int x = i * C::GT + gt, key = scale_key(j, i);
         rs[i] = 0.0f;
-        if (x < 2 * KT && key >= kb && key < ke && !(none >> (kk >> 4) & 1))
-          rs[i] = (x < KT ? p.k_scale : p.v_scale)[row_of(at, j, kk >> 4) + (kk & 15)];
+        if constexpr (KREG) {
+          const int g = x % KT >> 4;
+          int64_t row = off[0];
+#pragma unroll
+          for (int n = 1; n < C::NP; ++n) row += g >= n ? off[n] - off[n - 1] : 0;
+          if (x < 2 * KT && key >= kb && key < ke && !(bad >> g & 1))
+            rs[i] = (x < KT ? p.k_scale : p.v_scale)[row / C::ROWB + (x & 15)];
+        } else if (x < 2 * KT && key >= kb && key < ke && (unsigned)s_page[i] < (unsigned)p.n_pages) {
+          rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)s_page[i] * p.Hkv + h) << p.page_shift) + (key & page_mask)];
+        }
       }
+      if (j + 1 < nt) look_up_scales(j + 1);
     };
-    // rows as they lie, 64 chunks a load: these begin at a multiple of, and are at most, 16 rows
-    auto first_row = [&](int i) { return (i * C::GT + wr * 64) / C::CPR; };
-    auto issue_rows = [&](const void* cache, u32x4* to, int j, const int* at) {
+    // rows as they lie, 64 chunks a load
+    auto issue_rows = [&](const void* cache, u32x4* to, const int64_t* from) {
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-        const int64_t row = row_of(at, j, first_row(i) >> 4) + (first_row(i) & 15);
-        to[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(cache) + row * C::ROWB + lane * 16);
+        const char* at = static_cast<const char*>(cache);
+        if constexpr (C::KREG)
+          at += from[i * 64 / C::CPR / 16] + (i * 64 / C::CPR % 16) * C::ROWB;
+        else
+          at += from[i];
+        to[i] = *reinterpret_cast<const u32x4*>(at + (uint32_t)(lane * 16));
       }
     };
     // as the instruction takes K: lane l its key 32 b + (l & 31), chunk 2 i + (l >> 5)
-    auto issue_k = [&](int j) {
+    auto issue_k = [&]() {
 #pragma unroll
       for (int b = 0; b < C::KB; ++b) {
-        const char* at = static_cast<const char*>(p.k_cache) +
-                         (row_of(at_page, j, 2 * b + (ql >> 4)) + (ql & 15)) * C::ROWB + 16 * hh;
+        const char* at = static_cast<const char*>(p.k_cache) + (ql < 16 ? off[2 * b % C::NP] : off[(2 * b + 1) % C::NP]);
+        at += (ql & 15) * C::ROWB + 16 * hh;
 #pragma unroll
         for (int i = 0; i < C::CPR / 2; ++i) rk[b * (C::CPR / 2) + i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
       }
@@ -340,6 +367,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     const int c_lane = (wr * 64 + lane) % C::CPR, r_lane = (wr * 64 + lane) / C::CPR;
     // to LDS as bf16.  Rows outside the tile's range of keys become zeros; without a page (none: its bits) K becomes NaN,
     // and with it the scores of the rows that see it, V zeros.
+    auto page_no = [&](int i) { return KREG ? i * 64 / C::CPR / 16 : i; };  // of load i
     auto store_rows = [&](u32x4* from, int j, lds_bytes to, int row_bytes, unsigned none, bool is_k) {
       const int k0 = key_of(j);
       const lds_bytes at = to + r_lane * row_bytes + c_lane * (C::QUANT ? 32 : 16);
@@ -349,7 +377,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
         for (int i = 0; i < C::NL; ++i) {
           const int key = k0 + r_lane + i * STEP;
-          const bool out = key < kb || key >= ke, no_page = (none >> (first_row(i) >> 4) & 1) && !out;
+          const bool out = key < kb || key >= ke, no_page = (none >> page_no(i) & 1) && !out;
           // codes have no NaN in all types: theirs is put in below
           const uint32_t v = no_page && is_k && !C::QUANT ? 0x7fc07fc0u : 0u;
           if (out || no_page) from[i] = u32x4{v, v, v, v};
@@ -372,7 +400,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         for (int i = 0; i < C::NL; ++i) {
           const int key = k0 + r_lane + i * STEP;
           if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
-          if ((none >> (first_row(i) >> 4) & 1) && key >= kb && key < ke)
+          if ((none >> page_no(i) & 1) && key >= kb && key < ke)
             lds_as<u32x4>(at + i * STEP * row_bytes)[0] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
         }
       }
@@ -531,13 +559,14 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     if constexpr (C::KREG) {
       // a wave alone: the next tile is in flight from the end of this one's store on
       auto issue = [&](int j) {
-        find_pages(j);
-        issue_k(j);
-        if constexpr (C::QUANT) issue_scales(j, at_page, bad);
-        issue_rows(p.v_cache, rv, j, at_page);
+        find_rows(j);
+        issue_k();
+        if constexpr (C::QUANT) issue_scales(j);
+        issue_rows(p.v_cache, rv, off);
       };
       if (nt > 0) {
         look_up(0);
+        if constexpr (C::QUANT) look_up_scales(0);
         issue(0);
       }
       for (int j = 0; j < nt; ++j) {
@@ -559,21 +588,22 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     } else if (nt > 0) {
       // Scores run a tile ahead, so that their products and the exponentials of the tile before lie side by side.  Step
       // j: LDS holds K of tile j + 1 and V of tile j, K of j + 2 and V of j + 1 are in flight.
-      int v_page[C::NP];
+      int64_t v_off[C::NP];
       unsigned vbad = 0;
       auto next_k = [&](int j) {
-        find_pages(j);
-        issue_rows(p.k_cache, rk, j, at_page);
+        find_rows(j);
+        issue_rows(p.k_cache, rk, off);
       };
       auto to_v = [&]() {  // V follows K by a tile
 #pragma unroll
-        for (int g = 0; g < C::NP; ++g) v_page[g] = at_page[g];
+        for (int i = 0; i < C::NP; ++i) v_off[i] = off[i];
         vbad = bad;
       };
       auto next_v = [&](int j) {
-        issue_rows(p.v_cache, rv, j, v_page);
-        if constexpr (C::QUANT) issue_scales(j, v_page, vbad);
+        issue_rows(p.v_cache, rv, v_off);
+        if constexpr (C::QUANT) issue_scales(j);
       };
+      if constexpr (C::QUANT) look_up_scales(0);
       look_up(0);
       next_k(0), to_v(), next_v(0);
       store_k(0, 0, bad), store_v(0, 0, vbad);
@@ -588,6 +618,42 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       f32x16 x[C::KB] = {};
       if (wave_live) scores(0, x);
       sync();
+      if constexpr (C::TWO) {
+        // Each SIMD has a wave of either group: one is at its matrix products (the scores of the next tile and this
+        // tile's P V) while the other is at its exponentials, stores and loads; barriers keep them half a step apart.
+        // Three tiles in LDS: what one group stores in its half no wave of the other still reads.
+        int at = 0, next = 1, after = 2;
+        const bool second = wr >= 4;
+        if (second) sync();
+        auto step = [&](int j, auto last) {
+          if (wave_live) {
+            maximum(key_of(j), at, x);
+            weights(at, x, hi, lo);
+          }
+          if constexpr (!decltype(last)::value) {
+            if (j + 2 < nt) store_k(j + 2, after, bad);
+            store_v(j + 1, next, vbad);
+            if constexpr (C::QUANT) store_scales(next);
+            if (j + 2 < nt) to_v(), next_v(j + 2);
+            if (j + 3 < nt) next_k(j + 3);
+          }
+          sync();
+          if (wave_live) {
+            if constexpr (!decltype(last)::value) {
+#pragma unroll
+              for (int b = 0; b < C::KB; ++b) x[b] = f32x16{};
+              scores(next, x);
+            }
+            product(at, hi, lo);
+          }
+          sync();
+          const int t = at;
+          at = next, next = after, after = t;
+        };
+        for (int j = 0; j < nt - 1; ++j) step(j, std::false_type());
+        step(nt - 1, std::true_type());
+        if (!second) sync();
+      } else {
       auto step = [&](int j, auto last) {
         const int buf = j & 1;
         if (wave_live) {
@@ -611,6 +677,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       };
       for (int j = 0; j < nt - 1; ++j) step(j, std::false_type());
       step(nt - 1, std::true_type());
+      }
     }
     l = halves_sum(l);
 
@@ -667,6 +734,11 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 
     // ---- to memory: blocks d0 .. d0 + nd - 1 of O (in v) of the lanes' rows
     const bool to_slot = STREAM && !whole;
+    if (STREAM && unit_lo == 0 && !whole && threadIdx.x == 0) {
+      const int64_t last = u + units - 1;  // the item's last unit
+      reinterpret_cast<Part*>(p.partial)[blockIdx.x] = {(int)(last / share) - (int)blockIdx.x + 1,
+                                                        min(n_rows - r0, C::R), r0, q.q0, h, {0, 0, 0}};
+    }
     float* slot = STREAM ? slot_at<C>(p, 2 * blockIdx.x + (unit_lo == 0 ? 1 : 0)) : nullptr;
     const int srow = wr * 32 + ql;  // row in the tile
     auto put4 = [&](int d, const float* v, float inv) {  // elements d .. d + 3
@@ -746,72 +818,80 @@ __global__ __launch_bounds__(C::THREADS, C::D == 256 ? 1 : 2) void attention_ker
 // ---- host
 // How a call is cut, by its sizes alone.
 struct Plan {
-  bool few;     // up to 32 rows of a sequence: its keys are dealt over the waves of a workgroup
+  int rows;     // of a workgroup: 32, whose keys are dealt over its waves, 128 or 256
   bool stream;  // equal shares of all keys instead of one workgroup per row tile
-  int grid, min_units, rows;
+  int grid, min_units;
 };
-inline Plan plan_of(int T, int S, int Hq, int Hkv, int D, int64_t max_keys) {
+inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_keys) {
   const int64_t G = Hq / Hkv;
   Plan p;
-  p.few = T * G <= 32 * (int64_t)S;
-  p.rows = p.few ? 32 : 128;
-  const int unit = p.few ? (D == 64 ? 256 : 128) : (D == 256 ? 32 : 64);
+  const bool few = T * G <= 32 * (int64_t)S;
+  auto items_of = [&](int rows) { return (T * G + rows - 1) / rows * Hkv; };
+  p.rows = few ? 32 : D == 128 && type == MOE_BF16 && items_of(256) >= 512 ? 256 : 128;
+  const int unit = few ? (D == 64 ? 256 : 128) : 64;
   const int64_t tiles = T * G / p.rows + S;  // or fewer
   const int64_t units = (max_keys + 63 + unit - 1) / unit;
-  const int64_t items = (T * G + p.rows - 1) / p.rows * Hkv;
-  p.min_units = p.few ? 1 : 4;
-  p.stream = p.few ? max_keys > 2 * unit : items < 384 && units > 2 * p.min_units;
+  p.min_units = few ? 1 : 4;
+  p.stream = few ? max_keys > 2 * unit : items_of(128) < 384 && units > 2 * p.min_units;
   const int64_t all = tiles * Hkv * (p.stream ? (units + p.min_units - 1) / p.min_units : 1);
   const int64_t most = D == 256 ? 256 : 512;
   p.grid = (int)(p.stream && all > most ? most : all);
   return p;
 }
 
-// Joins the partial results of the items that more than one workgroup computed; grid and min_units as the launch
-// before, in x.  Workgroup w handles the item that begins in workgroup w's share and ends behind it.
+// Joins the partial results of the items that more than one workgroup computed; grid.x as in the launch before.  A row is
+// a workgroup's, its parts dealt over the waves.  Two rounds of loads, the parts' maxima and sums and then their O, each
+// some 1 us: two contexts of 131072 (64 parts a row) ... us.
 template <class C>
-__global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p, int min_units) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto weight = [&](int i) { return seq_work<C>(p, i); };
-  const int64_t total = sum_all(p.S, lane, weight);
-  const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
-  const int64_t u = blockIdx.x * per, u_end = u + per;
-  if (u_end >= total) return;
-  int64_t before;
-  const int s = find(p.S, lane, u_end - 1, weight, before);
-  const Seq q = seq_at<scalar_ptr>(p, s);
-  const int units = seq_units<C>(p, q), tiles = row_tiles<C>(p, q);
-  const int64_t item = (u_end - 1 - before) / units, begin = before + item * units, end = begin + units;
-  if (begin < u || end <= u_end) return;
-  const int h = (int)(item / tiles), m = (int)(item - (int64_t)h * tiles);
-  const int n_rows = min(q.n * p.G - m * C::R, C::R);
-  const int first = (int)blockIdx.x, n = (int)((end - 1) / per) - first + 1;  // workgroups that hold a part
+__global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
+  constexpr int E = C::D / 64, MOST = 512;
+  __shared__ float weight[MOST], sums[4][C::D];
+  const Part t = reinterpret_cast<const Part*>(p.partial)[blockIdx.x];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = (int)blockIdx.x;
   auto part = [&](int i) { return slot_at<C>(p, i == 0 ? 2 * first + 1 : 2 * (first + i)); };
-  constexpr int E = C::D / 64;
-  for (int r = blockIdx.y * 4 + wave; r < n_rows; r += gridDim.y * 4) {
-    float top = kNegInf;
-    for (int i = lane; i < n; i += 64) top = fmaxf(top, part(i)[C::R * C::D + 2 * r]);
+  for (int r = blockIdx.y; r < (t.n > 0 ? t.rows : 0); r += gridDim.y) {
+    float top = kNegInf, sum = 0.0f;
+    float2 ml[MOST / 64];
+#pragma unroll
+    for (int i = 0; i < MOST / 64; ++i) {
+      ml[i] = make_float2(kNegInf, 0.0f);
+      if (i * 64 < t.n && i * 64 + lane < t.n)
+        ml[i] = *reinterpret_cast<const float2*>(part(i * 64 + lane) + (size_t)C::R * C::D + 2 * r);
+      top = fmaxf(top, ml[i].x);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     const float sub = top == kNegInf ? 0.0f : top;
-    float sum = 0.0f, v[E] = {};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* a = part(i);
-      const float2 ml = *reinterpret_cast<const float2*>(a + (size_t)C::R * C::D + 2 * r);
-      const float f = exp2_fast(ml.x - sub);
-      sum += ml.y * f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] += a[(size_t)r * C::D + lane * E + e] * f;
+    for (int i = 0; i < MOST / 64; ++i) {
+      const float f = exp2_fast(ml[i].x - sub);
+      sum += ml[i].y * f;
+      if (wave == 0 && i * 64 < t.n) weight[i * 64 + lane] = f;
     }
-    const int row = m * C::R + r, tok = row / p.G, head = h * p.G + row - tok * p.G;
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    uint16_t* out = p.out + (q.q0 + tok) * p.out_ld + (int64_t)head * C::D + lane * E;
+    sum = wave_sum(sum);
+    __syncthreads();
+    float v[E] = {};
+#pragma unroll 8
+    for (int i = wave; i < t.n; i += 4) {
+      const float* a = part(i) + (size_t)r * C::D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = (uint16_t)cvt_bf16x2(v[e] * inv, 0.0f);
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)(q.q0 + tok) * p.Hq + head] =
+      for (int e = 0; e < E; ++e) v[e] += a[e] * weight[i];
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = v[e];
+    __syncthreads();
+    const int row = t.row0 + r, tok = row / p.G, head = t.h * p.G + row - tok * p.G;
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    if (threadIdx.x < C::D) {
+      const int d = threadIdx.x;
+      const float o = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
+      p.out[(t.q0 + tok) * p.out_ld + (int64_t)head * C::D + d] = (uint16_t)cvt_bf16x2(o * inv, 0.0f);
+    }
+    if (p.lse && threadIdx.x == 0)
+      p.lse[(int64_t)(t.q0 + tok) * p.Hq + head] =
           sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+    __syncthreads();
   }
 }
 
@@ -830,15 +910,19 @@ hipError_t run(const AttentionArgs& a, const Plan& plan, hipStream_t st) {
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
   kernel<<<plan.grid, C::THREADS, C::LDS, st>>>(a, plan.min_units);
-  if (STREAM && plan.grid > 1) combine_kernel<C><<<dim3(plan.grid, 4), 256, 0, st>>>(a, plan.min_units);
+  if (STREAM && plan.grid > 1) combine_kernel<C><<<dim3(plan.grid, C::R / 4), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <int D, int CT>
 hipError_t run_type(const AttentionArgs& a, const Plan& plan, hipStream_t st) {
   using Few = Cfg<D, CT, 1, 4, D == 64 ? 64 : 32>;
-  using Many = Cfg<D, CT, 4, 1, D == 256 ? 32 : 64>;
-  if (plan.few) return plan.stream ? run<Few, true>(a, plan, st) : run<Few, false>(a, plan, st);
+  using Many = Cfg<D, CT, 4, 1, 64>;
+  if (plan.rows == 32) return plan.stream ? run<Few, true>(a, plan, st) : run<Few, false>(a, plan, st);
+  if constexpr (D == 128 && CT == MOE_BF16) {
+    using Wide = Cfg<D, CT, 8, 1, 64>;
+    if (plan.rows == 256) return run<Wide, false>(a, plan, st);
+  }
   return plan.stream ? run<Many, true>(a, plan, st) : run<Many, false>(a, plan, st);
 }
 
