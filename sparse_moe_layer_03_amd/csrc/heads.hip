@@ -1,12 +1,15 @@
 // Heads of q, k and v rows: norm of each head, rotary positions, and the paged cache's write and read.
 //
-// A head of D elements is a group of LPH lanes (8, 16 or 32) with a 16-byte chunk each.  All is bound by the rows'
-// bytes.  The angle of a pair i at position p is the fraction of p * freq[i] turns: the product is taken in 64 bits
-// (in 32 a position of 10^6 would leave the angle of the fastest pair 0.06 rad off), its sine and cosine in 32.  A
-// workgroup works them out once per token for all heads, into LDS.
+// A head of D elements is a group of LPH lanes (8, 16 or 32) with a 16-byte chunk each.  A group works on heads of one
+// token, so that the sines and cosines of its chunk's pairs stay in registers; what lanes exchange (sums, maxima, the
+// other half of a rotated pair) goes by lane permutations.  No LDS and no barriers in the usual layouts.  (With a table
+// of a token's sines in LDS and sums by LDS permutes 8192 tokens of 16 + 16 heads took 54 us, ... now.)
 //
-// Quantisation of a row as in moe_quantize_i8: a = max(max |x|, 2^-100), scale = a / top, code = x (top / a) rounded to
-// nearest, top = 127 or 448; a row that holds Inf or NaN gets scale NaN and codes 0.
+// The angle of a pair i at position p is the fraction of p * freq[i] turns: the product is taken in 64 bits (in 32 a
+// position of 10^6 would leave the angle of the fastest pair 0.06 rad off), its sine and cosine in 32.
+//
+// Quantisation of a row as in moe_quantize_i8: a = max(max |x|, 2^-100), scale = a / top, code = x / scale rounded to
+// nearest, top = 127 or 448 (by reciprocals of 1 ulp); a row that holds Inf or NaN gets scale NaN and codes 0.
 #include "attend_internal.h"
 
 namespace moe {
@@ -15,20 +18,38 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;  // heads whose loads a lane has in flight
 
-// LDS written by some lanes of a wave and read by others of it: in order, and the compiler keeps it so.
-__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
-
-template <int LPH>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < LPH; d <<= 1) v += __shfl_xor(v, d);
+template <int CTRL, int BANKS = 0xf>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xf, BANKS, false));
+}
+// The lanes 16 apart within pairs of rows: (row 0, row 0, row 2, row 2) and (row 1, row 1, row 3, row 3).
+__device__ __forceinline__ void rows_apart(float v, float& even, float& odd) {
+  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  even = __uint_as_float(x[0]), odd = __uint_as_float(x[1]);
+}
+// All-lane reduction over groups of LPH lanes: neighbours, pairs, quads mirrored, eights mirrored, rows.
+template <int LPH, class F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  v = f(v, dpp<0xb1>(v, v));
+  v = f(v, dpp<0x4e>(v, v));
+  v = f(v, dpp<0x141>(v, v));
+  if constexpr (LPH > 8) v = f(v, dpp<0x140>(v, v));
+  if constexpr (LPH > 16) {
+    float a, b;
+    rows_apart(v, a, b);
+    v = f(a, b);
+  }
   return v;
 }
+// The value of the lane LPH / 2 away.
 template <int LPH>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < LPH; d <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  return v;
+__device__ __forceinline__ float other_half(float v, int c) {
+  if constexpr (LPH == 16) return dpp<0x128>(v, v);
+  if constexpr (LPH == 8) return dpp<0x12c, 0x5>(dpp<0x124, 0xa>(v, v), v);
+  float a, b;
+  rows_apart(v, a, b);
+  return c < LPH / 2 ? b : a;
 }
 
 __device__ __forceinline__ u32x4 pack8(const float* f) {
@@ -38,146 +59,170 @@ __device__ __forceinline__ u32x4 pack8(const float* f) {
   return v;
 }
 
-template <int LPH>
-__global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int tokens) {
-  constexpr int G = kThreads / LPH;  // heads at work at once
-  __shared__ float stage[8][kThreads];
-  extern __shared__ float2 table[];  // [tokens][8][stride]: cosine and sine of pair i at [i & 7][i >> 3]
-  const int tid = threadIdx.x, c = tid % LPH, group = tid / LPH;
-  const int units = p.Hq + 2 * p.Hkv;
-  const int64_t t0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * tokens;
-  if (t0 >= p.T) return;
-  const int nt = (int)min((int64_t)tokens, p.T - t0), total = nt * units;
-  const int half = p.rot / 2, stride = (half + 7) / 8;
+// How pairs lie: within a chunk, in chunks LPH / 2 lanes apart (the whole head in halves), in chunks some lanes apart,
+// anywhere.
+enum { kInside, kWhole, kApart, kOdd };
+
+// TYPE: of the cache, -1 for none.  per_token: groups of a token.
+template <int LPH, int TYPE, int PAIRS>
+__global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int per_token) {
+  constexpr int G = kThreads / LPH;  // groups of a workgroup
+  __shared__ float stage[PAIRS == kOdd ? 8 : 1][PAIRS == kOdd ? kThreads : 1];
+  const int tid = threadIdx.x, c = tid % LPH;
+  const int64_t group = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * G + tid / LPH;
+  const int64_t t = group / per_token;
+  if (t >= p.T) return;
+  const int first = (int)(group - t * per_token);
+  const int units = TYPE < 0 ? p.Hq : p.Hq + 2 * p.Hkv;
+  const int half = p.rot / 2;
   const bool in = c * 8 < p.D;
 
-  struct Unit {
-    int tok, head, kind;  // kind 0: q, 1: k, 2: v
-    bool live;
-  };
-  auto unit = [&](int base, int u) {
-    const int i = base + u * G + group;
-    Unit n;
-    n.live = i < total;
-    n.tok = n.live ? i / units : 0;
-    const int j = n.live ? i - n.tok * units : 0;
-    n.kind = j < p.Hq ? 0 : j < p.Hq + p.Hkv ? 1 : 2;
-    n.head = n.kind == 0 ? j : n.kind == 1 ? j - p.Hq : j - p.Hq - p.Hkv;
-    return n;
-  };
-  auto load = [&](const Unit& n) {
+  auto load = [&](int j) {
     u32x4 w = {0u, 0u, 0u, 0u};
-    if (n.live && in) {
-      const int64_t t = t0 + n.tok;
-      const uint16_t* x = n.kind == 0 ? p.q + t * p.q_ld : n.kind == 1 ? p.k + t * p.k_ld : p.v + t * p.v_ld;
-      w = *reinterpret_cast<const u32x4*>(x + n.head * p.D + c * 8);
+    if (j < units && in) {
+      const uint16_t* x = p.q + t * p.q_ld + j * p.D;
+      if (TYPE >= 0 && j >= p.Hq)
+        x = j < p.Hq + p.Hkv ? p.k + t * p.k_ld + (j - p.Hq) * p.D : p.v + t * p.v_ld + (j - p.Hq - p.Hkv) * p.D;
+      w = *reinterpret_cast<const u32x4*>(x + c * 8);
     }
     return w;
   };
-
   u32x4 raw[kUnits];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) raw[u] = load(unit(0, u));
+  for (int u = 0; u < kUnits; ++u) raw[u] = load(first + u * per_token);
+
   float wq[8], wk[8];
   if (p.w_q && in) chunk_to_f32(*reinterpret_cast<const u32x4*>(p.w_q + c * 8), wq);
-  if (p.w_k && in) chunk_to_f32(*reinterpret_cast<const u32x4*>(p.w_k + c * 8), wk);
-  for (int i = tid; i < nt * half; i += kThreads) {
-    const int tok = i / half, pair = i - tok * half;
-    const double turns = (double)p.pos[t0 + tok] * p.freq[pair];
-    float s, co;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &co);
-    table[(tok * 8 + (pair & 7)) * stride + (pair >> 3)] = make_float2(co * p.mscale, s * p.mscale);
-  }
-  __syncthreads();
-
-  for (int base = 0; base < total; base += kUnits * G) {
-    if (base > 0) {
+  if (TYPE >= 0 && p.w_k && in) chunk_to_f32(*reinterpret_cast<const u32x4*>(p.w_k + c * 8), wk);
+  const int slot = TYPE >= 0 ? p.slots[t] : 0;
+  // sines and cosines of the chunk's elements (kInside: of its pairs); 1 and 0 behind the rotated part
+  constexpr int NC = PAIRS == kInside ? 4 : 8;
+  float co[NC], si[NC];
+  const bool lower = c * 8 < half;  // (unless kInside or kOdd) the chunk holds pairs' first elements
+  if (p.rot > 0) {
+    const double pos = (double)p.pos[t];
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) raw[u] = load(unit(base, u));
+    for (int e = 0; e < NC; ++e) {
+      const int i = PAIRS == kInside ? c * 4 + e : c * 8 + e;
+      const int pair = PAIRS == kInside || i < half ? i : i - half;
+      co[e] = 1.0f, si[e] = 0.0f;
+      if (PAIRS == kInside ? i < half : i < p.rot) {
+        const double turns = pos * p.freq[pair];
+        float sn, cs;
+        sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
+        co[e] = cs * p.mscale, si[e] = sn * p.mscale;
+        // the second element of a pair takes the first with the other sign
+        if (PAIRS != kInside && i < half) si[e] = -si[e];
+      }
     }
+  }
+
+  const float d_inv = 1.0f / (float)p.D;
+  const int64_t page_row = TYPE >= 0 ? ((int64_t)(slot >> p.page_shift) * p.Hkv << p.page_shift) +
+                                           (slot & ((1 << p.page_shift) - 1))
+                                     : 0;
+  const bool keep = TYPE >= 0 && (unsigned)slot < (unsigned)p.n_slots;
+  for (int j0 = first; j0 < units; j0 += kUnits * per_token) {
+    u32x4 ahead[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) ahead[u] = load(j0 + (kUnits + u) * per_token);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      if (base + u * G >= total) break;
-      const Unit n = unit(base, u);
+      const int j = j0 + u * per_token;
+      if (j >= units) break;
+      const int kind = TYPE < 0 || j < p.Hq ? 0 : j < p.Hq + p.Hkv ? 1 : 2;  // q, k, v
       float f[8];
       chunk_to_f32(raw[u], f);
-      const bool is_k = n.kind == 1;
-      if (n.kind == 0 ? p.w_q != nullptr : is_k && p.w_k != nullptr) {
+      if (kind == 0 ? p.w_q != nullptr : kind == 1 && p.w_k != nullptr) {
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += f[e] * f[e];
-        const float r = 1.0f / sqrtf(group_sum<LPH>(s) / (float)p.D + p.eps);
-        if (in)
+        s = group_reduce<LPH>(s, [](float a, float b) { return a + b; });
+        const float r = __builtin_amdgcn_rsqf(s * d_inv + p.eps);  // 1 ulp
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = f[e] * r * ((is_k ? wk[e] : wq[e]) + p.w_add);
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * r * ((kind == 1 ? wk[e] : wq[e]) + p.w_add);
+        if (!in)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 0.0f;
       }
-      if (p.rot > 0 && n.kind != 2) {
-        const float2* tab = table + n.tok * 8 * stride;
-        if (p.interleaved) {
+      if (p.rot > 0 && kind != 2) {
+        if constexpr (PAIRS == kInside) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int i = c * 4 + e / 2;
-            if (i < half) {
-              const float2 a = tab[(i & 7) * stride + (i >> 3)];
-              const float x = f[e], y = f[e + 1];
-              f[e] = x * a.x - y * a.y;
-              f[e + 1] = y * a.x + x * a.y;
+          for (int e = 0; e < 4; ++e) {
+            if (c * 4 + e < half) {
+              const float x = f[2 * e], y = f[2 * e + 1];
+              f[2 * e] = x * co[e] - y * si[e];
+              f[2 * e + 1] = y * co[e] + x * si[e];
             }
           }
+        } else if constexpr (PAIRS == kWhole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = f[e] * co[e] + other_half<LPH>(f[e], c) * si[e];
+        } else if constexpr (PAIRS == kApart) {
+          const int from = (tid & 63) + (lower ? half / 8 : -(half / 8));
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __shfl(f[e], from);
+          if (c * 8 < p.rot)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f[e] * co[e] + o[e] * si[e];
         } else {
-          wave_fence();
+          // (of one wave: in order)
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
           for (int e = 0; e < 8; ++e) stage[e][tid] = f[e];
-          wave_fence();
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int i = c * 8 + e;
             if (i < p.rot) {
-              const bool first = i < half;
-              const int pair = first ? i : i - half, other = first ? i + half : i - half;
-              const float2 a = tab[(pair & 7) * stride + (pair >> 3)];
-              const float o = stage[other & 7][tid - c + (other >> 3)];
-              f[e] = f[e] * a.x + (first ? -o : o) * a.y;
+              const int other = i < half ? i + half : i - half;
+              f[e] = f[e] * co[e] + stage[other & 7][tid - c + (other >> 3)] * si[e];
             }
           }
         }
       }
-      const int64_t t = t0 + n.tok;
-      if (n.kind == 0) {
-        if (n.live && in) *reinterpret_cast<u32x4*>(p.q_out + t * p.out_ld + n.head * p.D + c * 8) = pack8(f);
+      if (kind == 0) {
+        if (in) *reinterpret_cast<u32x4*>(p.q_out + t * p.out_ld + j * p.D + c * 8) = pack8(f);
         continue;
       }
-      const int slot = p.slots[t];
-      const bool write = n.live && (unsigned)slot < (unsigned)p.n_slots;
-      const int64_t row =
-          ((int64_t)(slot >> p.page_shift) * p.Hkv + n.head << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-      void* cache = is_k ? p.k_cache : p.v_cache;
-      if (p.type == MOE_BF16) {
-        if (write && in) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(cache) + row * p.D + c * 8) = pack8(f);
-        continue;
-      }
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
-      m = group_max<LPH>(m);
-      const bool bad = m >= 0x7f800000u;
-      const float a = fmaxf(__uint_as_float(m), kQuantTiny), top = p.type == MOE_I8 ? 127.0f : 448.0f;
-      const float inv = top / a;
-      u32x2 w = {0u, 0u};
-      if (p.type == MOE_I8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= ((uint32_t)__float2int_rn(f[e] * inv) & 0xffu) << (8 * (e & 3));
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
-          w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
+      if constexpr (TYPE >= 0) {
+        const int head = j - p.Hq - (kind == 2 ? p.Hkv : 0);
+        const int64_t row = page_row + ((int64_t)head << p.page_shift);
+        void* cache = kind == 1 ? p.k_cache : p.v_cache;
+        if constexpr (TYPE == MOE_BF16) {
+          if (keep && in) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(cache) + row * p.D + c * 8) = pack8(f);
+          continue;
         }
+        // the maximum of the magnitudes' bit patterns, ordered as they are, Inf and NaN above all finite ones
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+        m = __float_as_uint(group_reduce<LPH>(__uint_as_float(m), [](float a, float b) {
+          return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+        }));
+        const bool bad = m >= 0x7f800000u;
+        constexpr float top = TYPE == MOE_I8 ? 127.0f : 448.0f;
+        // (the reciprocal, 1 ulp, is taken of the scale: that of the largest floats is no normal one)
+        const float scale = fmaxf(__uint_as_float(m), kQuantTiny) * (1.0f / top), inv = __builtin_amdgcn_rcpf(scale);
+        u32x2 w = {0u, 0u};
+        if constexpr (TYPE == MOE_I8) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e >> 2] |= ((uint32_t)__float2int_rn(f[e] * inv) & 0xffu) << (8 * (e & 3));
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
+            w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
+          }
+        }
+        if (bad) w = u32x2{0u, 0u};
+        if (keep && in) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(cache) + row * p.D + c * 8) = w;
+        if (keep && c == 0) (kind == 1 ? p.k_scale : p.v_scale)[row] = bad ? __uint_as_float(0x7fc00000u) : scale;
       }
-      if (bad) w = u32x2{0u, 0u};
-      if (write && in) *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(cache) + row * p.D + c * 8) = w;
-      if (write && c == 0) (is_k ? p.k_scale : p.v_scale)[row] = bad ? __uint_as_float(0x7fc00000u) : a / top;
     }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) raw[u] = ahead[u];
   }
 }
 
@@ -192,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheReadArgs p) {
   const int slot = p.slots[r];
   if ((unsigned)slot >= (unsigned)p.n_slots) return;
   const int64_t row =
-      ((int64_t)(slot >> p.page_shift) * p.Hkv + head << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+      (((int64_t)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
   const void* cache = is_v ? p.v_cache : p.k_cache;
   const int64_t to = ((int64_t)r * p.Hkv + head) * p.D + c * 8;
   void* out = is_v ? p.v : p.k;
@@ -232,20 +277,43 @@ static dim3 grid_of(int64_t blocks) {
   return blocks <= (1 << 20) ? dim3((unsigned)blocks) : dim3(1u << 20, (unsigned)((blocks + (1 << 20) - 1) >> 20));
 }
 
-hipError_t launch_heads(const HeadArgs& a, hipStream_t st) {
-  const int lph = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
-  const int units = a.Hq + 2 * a.Hkv, at_once = kThreads / lph;
-  // tokens of a workgroup: enough heads for its lanes, as long as there are workgroups for every CU
-  int tokens = 1;
-  while (tokens * units < kUnits * at_once && a.T / tokens > 2048 && tokens < 16) tokens *= 2;
-  const size_t lds = (size_t)tokens * 8 * ((a.rot / 2 + 7) / 8) * sizeof(float2);
-  const dim3 blocks = grid_of((a.T + tokens - 1) / tokens);
-  if (lph == 8)
-    heads_kernel<8><<<blocks, kThreads, lds, st>>>(a, tokens);
-  else if (lph == 16)
-    heads_kernel<16><<<blocks, kThreads, lds, st>>>(a, tokens);
+template <int LPH, int TYPE>
+static void heads_pairs(const HeadArgs& a, int per_token, dim3 grid, hipStream_t st) {
+  if (a.interleaved || a.rot == 0)
+    heads_kernel<LPH, TYPE, kInside><<<grid, kThreads, 0, st>>>(a, per_token);
+  else if (a.rot == 8 * LPH)
+    heads_kernel<LPH, TYPE, kWhole><<<grid, kThreads, 0, st>>>(a, per_token);
+  else if (a.rot % 16 == 0)
+    heads_kernel<LPH, TYPE, kApart><<<grid, kThreads, 0, st>>>(a, per_token);
   else
-    heads_kernel<32><<<blocks, kThreads, lds, st>>>(a, tokens);
+    heads_kernel<LPH, TYPE, kOdd><<<grid, kThreads, 0, st>>>(a, per_token);
+}
+
+template <int LPH>
+static void heads_type(const HeadArgs& a, hipStream_t st) {
+  constexpr int G = kThreads / LPH;
+  // groups of a token: as many as fill the CUs (2^15 groups of 16 lanes), at most one per head
+  const int units = a.Hq + 2 * a.Hkv;
+  const int64_t want = ((int64_t)(1 << 19) / LPH + a.T - 1) / a.T;
+  const int per_token = (int)(want < units ? want : units);
+  const dim3 grid = grid_of(((int64_t)a.T * per_token + G - 1) / G);
+  if (a.Hkv == 0)
+    heads_pairs<LPH, -1>(a, per_token, grid, st);
+  else if (a.type == MOE_I8)
+    heads_pairs<LPH, MOE_I8>(a, per_token, grid, st);
+  else if (a.type == MOE_E4M3)
+    heads_pairs<LPH, MOE_E4M3>(a, per_token, grid, st);
+  else
+    heads_pairs<LPH, MOE_BF16>(a, per_token, grid, st);
+}
+
+hipError_t launch_heads(const HeadArgs& a, hipStream_t st) {
+  if (a.D <= 64)
+    heads_type<8>(a, st);
+  else if (a.D <= 128)
+    heads_type<16>(a, st);
+  else
+    heads_type<32>(a, st);
   return hipGetLastError();
 }
 
