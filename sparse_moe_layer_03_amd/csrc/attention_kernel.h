@@ -103,9 +103,9 @@ __device__ __forceinline__ int row_tiles(const AttentionArgs& p, const Seq& q) {
   return (int)(((int64_t)q.n * p.G + C::R - 1) / C::R);
 }
 // Units of work of a sequence: all its row tiles and key heads times its keys.
-template <class C>
+template <class C, class PTR>
 __device__ __forceinline__ int64_t seq_work(const AttentionArgs& p, int s) {
-  const Seq q = seq_at<const int32_t*>(p, s);
+  const Seq q = seq_at<PTR>(p, s);
   return (int64_t)p.Hkv * row_tiles<C>(p, q) * seq_units<C>(p, q);
 }
 
@@ -121,21 +121,14 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)v, lane), hi = __builtin_amdgcn_readlane((int)(v >> 32), lane);
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-// Sum of weight(s) over all sequences.
-template <class W>
-__device__ __forceinline__ int64_t sum_all(int S, int lane, W weight) {
-  if (S == 1) return lane_value(weight(0), 0);
-  int64_t sum = 0;
-  for (int b = 0; b < S; b += 64) sum += b + lane < S ? weight(b + lane) : 0;
-  return lane_value(wave_scan(sum, lane), 63);
-}
-// The sequence in which the running sum of weights passes `at`, and the sum before it; S if none does.
+// The sequence in which the running sum of weights passes `at`, and the sum before it; S if none does.  weight(s, PTR):
+// of a sequence of the lane's own (const int32_t*) or the same in all (scalar_ptr).
 template <class W>
 __device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64_t& before) {
   before = 0;
-  if (S == 1) return at < lane_value(weight(0), 0) ? 0 : 1;
+  if (S == 1) return at < weight(0, scalar_ptr()) ? 0 : 1;
   for (int b = 0; b < S; b += 64) {
-    const int64_t incl = before + wave_scan(b + lane < S ? weight(b + lane) : 0, lane);
+    const int64_t incl = before + wave_scan(b + lane < S ? weight(b + lane, (const int32_t*)nullptr) : 0, lane);
     const int n = __popcll(__ballot(incl <= at));
     if (n < 64) {
       if (n > 0) before = lane_value(incl, n - 1);
@@ -144,6 +137,28 @@ __device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64
     before = lane_value(incl, 63);
   }
   return S;
+}
+// Share `index` of `shares` equal ones (none below `least`) of all weights: its begin and end, and as `find` for its begin.
+template <class W>
+__device__ __forceinline__ int find_share(int S, int lane, int index, int shares, int least, W weight, int64_t& share,
+                                          int64_t& begin, int64_t& end, int64_t& before) {
+  int64_t total = 0, incl = 0;  // incl: of up to 64 sequences, one pass over them for both steps
+  if (S == 1) {
+    total = weight(0, scalar_ptr());
+  } else {
+    int64_t sum = 0;
+    for (int b = 0; b < S; b += 64) sum += b + lane < S ? weight(b + lane, (const int32_t*)nullptr) : 0;
+    incl = wave_scan(sum, lane);
+    total = lane_value(incl, 63);
+  }
+  share = max((total + shares - 1) / shares, (int64_t)least);
+  begin = index * share, end = min(total, begin + share);
+  before = 0;
+  if (S == 1 || begin >= end) return 0;
+  if (S > 64) return find(S, lane, begin, weight, before);
+  const int n = __popcll(__ballot(incl <= begin));
+  if (n > 0) before = lane_value(incl, n - 1);
+  return n;
 }
 
 // Scores and sums are kept by lane halves; both halves' maximum or sum.
@@ -213,17 +228,12 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
   int64_t u = 0, u_end = 1, before = 0, share = 1;
   int s, h = 0, m = 0;
   if constexpr (STREAM) {
-    auto weight = [&](int i) { return seq_work<C>(p, i); };
-    const int64_t total = sum_all(p.S, lane0, weight);
-    const int64_t per = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)min_units);
-    u = blockIdx.x * per, u_end = min(total, u + per);
+    auto weight = [&](int i, auto ptr) { return seq_work<C, decltype(ptr)>(p, i); };
+    s = find_share(p.S, lane0, blockIdx.x, gridDim.x, min_units, weight, share, u, u_end, before);
     // (written again below where there is such an item)
     if (threadIdx.x == 0) reinterpret_cast<Part*>(p.partial)[blockIdx.x].n = 0;
-    if (u >= u_end) return;
-    share = per;
-    s = find(p.S, lane0, u, weight, before);
   } else {
-    auto weight = [&](int i) { return (int64_t)row_tiles<C>(p, seq_at<const int32_t*>(p, i)); };
+    auto weight = [&](int i, auto ptr) { return (int64_t)row_tiles<C>(p, seq_at<decltype(ptr)>(p, i)); };
     // the last tiles, which see the most keys, first
     const int64_t tiles = gridDim.x / p.Hkv;
     h = blockIdx.x % p.Hkv;
@@ -844,13 +854,55 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
 // some 1 us: two contexts of 131072 (64 parts a row) ... us.
 template <class C>
 __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
-  constexpr int E = C::D / 64, MOST = 512;
+  constexpr int E = C::D / 64, MOST = 512, FEW = 8;
   __shared__ float weight[MOST], sums[4][C::D];
   const Part t = reinterpret_cast<const Part*>(p.partial)[blockIdx.x];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = (int)blockIdx.x;
   auto part = [&](int i) { return slot_at<C>(p, i == 0 ? 2 * first + 1 : 2 * (first + i)); };
-  for (int r = blockIdx.y; r < (t.n > 0 ? t.rows : 0); r += gridDim.y) {
+  auto put = [&](int r, int d, float o, float inv) {
+    const int row = t.row0 + r, tok = row / p.G, head = t.h * p.G + row - tok * p.G;
+    p.out[(t.q0 + tok) * p.out_ld + (int64_t)head * C::D + d] = (uint16_t)cvt_bf16x2(o * inv, 0.0f);
+  };
+  auto put_lse = [&](int r, float top, float sum) {
+    const int row = t.row0 + r, tok = row / p.G, head = t.h * p.G + row - tok * p.G;
+    p.lse[(int64_t)(t.q0 + tok) * p.Hq + head] =
+        sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+  };
+  const int rows = t.n > 0 ? t.rows : 0;
+  if (t.n <= FEW) {
+    // few parts: a row is a wave's
+    for (int r = blockIdx.y * 4 + wave; r < rows; r += gridDim.y * 4) {
+      float2 ml = make_float2(kNegInf, 0.0f);
+      if (lane < t.n) ml = *reinterpret_cast<const float2*>(part(lane) + (size_t)C::R * C::D + 2 * r);
+      float v[FEW][E];
+#pragma unroll
+      for (int i = 0; i < FEW; ++i)
+        if (i < t.n)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[i][e] = part(i)[(size_t)r * C::D + lane + 64 * e];
+      float top = ml.x;
+#pragma unroll
+      for (int d = 1; d < FEW; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      top = __shfl(top, 0);
+      const float f = exp2_fast(ml.x - (top == kNegInf ? 0.0f : top));
+      const float sum = wave_sum(ml.y * f);
+      float o[E] = {};
+#pragma unroll
+      for (int i = 0; i < FEW; ++i)
+        if (i < t.n) {
+          const float fi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i));
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += v[i][e] * fi;
+        }
+      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) put(r, lane + 64 * e, o[e], inv);
+      if (p.lse && lane == 0) put_lse(r, top, sum);
+    }
+    return;
+  }
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     float top = kNegInf, sum = 0.0f;
     float2 ml[MOST / 64];
 #pragma unroll
@@ -881,16 +933,12 @@ __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = v[e];
     __syncthreads();
-    const int row = t.row0 + r, tok = row / p.G, head = t.h * p.G + row - tok * p.G;
     const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     if (threadIdx.x < C::D) {
       const int d = threadIdx.x;
-      const float o = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
-      p.out[(t.q0 + tok) * p.out_ld + (int64_t)head * C::D + d] = (uint16_t)cvt_bf16x2(o * inv, 0.0f);
+      put(r, d, (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]), inv);
     }
-    if (p.lse && threadIdx.x == 0)
-      p.lse[(int64_t)(t.q0 + tok) * p.Hq + head] =
-          sum > 0.0f || sum != sum ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+    if (p.lse && threadIdx.x == 0) put_lse(r, top, sum);
     __syncthreads();
   }
 }
