@@ -529,10 +529,18 @@ def _cache(k_cache, v_cache, k_scale, v_scale, n_pages, Hkv, P, D):
     types = _cache_types()
     if dtype not in types:
         raise ValueError(f"k_cache is {dtype}; expected {', '.join(map(str, types))}")
-    shape = (n_pages, Hkv, P, D)
-    if k_scale is None and v_scale is None:
-        return types[dtype], _args(("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape)) + [None, None]
-    scales = (n_pages, Hkv, P)
+    shape, scales = (n_pages, Hkv, P, D), (n_pages, Hkv, P)
+    # what _args checks, in one expression where all is as it should be
+    if (v_cache.__class__ is k_cache.__class__ and v_cache.dtype is dtype and k_cache.shape == v_cache.shape == shape
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_cache.get_device() == v_cache.get_device() == (dev := _device())):
+        if k_scale is None and v_scale is None:
+            return types[dtype], (k_cache.data_ptr(), v_cache.data_ptr(), None, None)
+        if (k_scale.__class__ is v_scale.__class__ is k_cache.__class__
+                and k_scale.dtype is v_scale.dtype is torch.float32 and k_scale.shape == v_scale.shape == scales
+                and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and k_scale.get_device() == v_scale.get_device() == dev):
+            return types[dtype], (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
     return types[dtype], _args(
         ("k_cache", k_cache, dtype, shape), ("v_cache", v_cache, dtype, shape),
         ("k_scale", k_scale, torch.float32, scales), ("v_scale", v_scale, torch.float32, scales))
