@@ -40,7 +40,82 @@ class Shapes:
     I_s: int
 
 
-class DeviceLayer:
+class _Resident:
+    """What keeps weights and a workspace on one GPU: the workspace's life over streams and captured graphs, outputs in
+    their streams' pools, and checks of tensors against the device.  A class of it has ``device``, ``_home`` (a tensor
+    there) and ``_width`` (columns of an output)."""
+
+    def _init_workspace(self):
+        self._ws = None
+        self._ws_bytes = 0
+        self._ws_streams = []  # handles of the streams the current workspace has been used on since it was allocated
+        self._ws_captured = False  # whether a captured call has used it
+        self._ws_kept = []  # earlier workspaces that graphs still write on replay
+
+    def _reserve(self, need: int):
+        import torch
+        if self._ws is None or self._ws_bytes < need:
+            if self._ws is not None:
+                # the caching allocator tracks only the allocating stream: keep the old buffer from being
+                # handed out again before work already enqueued on the other streams that used it is done
+                for st in self._ws_streams:
+                    self._ws.record_stream(torch.cuda.ExternalStream(st, device=self.device))
+                if self._ws_captured:
+                    self._ws_kept.append(self._ws)
+            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            self._ws_bytes = max(need, 256)
+            self._ws_streams = []
+            self._ws_captured = False
+        return self._ws, self._ws_bytes
+
+    def _pool(self, stream):
+        """The context in which memory for work on ``stream`` (None, a torch stream or a raw handle) is allocated: a
+        block of the current stream's pool may still be in use by work pending there."""
+        import torch
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int)
+                                 else stream)
+
+    def _output(self, T: int, stream):
+        """[T, width] for the kernels on ``stream`` to write; once dropped, reused only behind the current stream's work at
+        that time, which may read it."""
+        import torch
+        with self._pool(stream):
+            y = torch.empty((T, self._width), dtype=torch.bfloat16, device=self.device)
+        if stream is not None:
+            y.record_stream(torch.cuda.current_stream(self.device))
+        return y
+
+    def _note_stream(self, stream):
+        """Remember what the workspace is used by: the stream (None, a torch stream or a raw handle), a capture."""
+        import torch
+        st = moe._stream(stream)
+        if st not in self._ws_streams:
+            self._ws_streams.append(st)
+        if not self._ws_captured:
+            with self._pool(stream):
+                self._ws_captured = torch.cuda.is_current_stream_capturing()
+
+    def _check_tensors(self, *tensors):
+        """Refuses, before anything is enqueued, tensors given as (name, tensor, shapes, dtypes) that the kernels would
+        misread or write astray: another shape, type, order or device than the layer's, which is the current one."""
+        at = self._home.get_device()
+        for name, t, shapes, dtypes in tensors:
+            if t.dtype in dtypes and t.shape in shapes and t.is_contiguous() and t.get_device() == at >= 0:
+                continue
+            if t.dtype not in dtypes:
+                raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(map(str, dtypes))}")
+            if t.shape not in shapes:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            raise ValueError(f"{name} is on {t.device}, the layer on {self._home.device}")
+        if at != moe._device():
+            raise ValueError(f"the layer is on GPU {at}; the current one is {moe._device()}")
+
+
+class DeviceLayer(_Resident):
     """The layer's weights on one GPU plus a reusable workspace.
 
     ``fp8``: also upload the FP8 expert weights (``<key>_fp8`` codes and
@@ -87,14 +162,18 @@ class DeviceLayer:
         E, I, H = weights["w_gate"].shape
         I_s = 0 if weights.get("ws_gate") is None else weights["ws_gate"].shape[0]
         self.shapes = Shapes(H=H, E=E, k=k, I=I, I_s=I_s)
-        self._ws = None
-        self._ws_bytes = 0
-        self._ws_streams = []  # handles of the streams the current workspace has been used on since it was allocated
-        self._ws_captured = False  # whether a captured call has used it
-        self._ws_kept = []  # earlier workspaces that graphs still write on replay
+        self._init_workspace()
         self._i8_views = None  # (workspace address, T, the views forward uses) of 8-bit layers
         if i8:
             self._quantize_weights()
+
+    @property
+    def _home(self):
+        return self.w["w_router"]
+
+    @property
+    def _width(self):
+        return self.shapes.H
 
     @classmethod
     def from_inputs(cls, inp, device="cuda:0", fp8: bool = False, q4: bool = False, i8: bool = False):
@@ -133,68 +212,6 @@ class DeviceLayer:
         if need == 0 and T > 0:
             raise moe.MoEError(moe.MOE_ERR_SHAPE, "unsupported shapes")
         return self._reserve(need)
-
-    def _reserve(self, need: int):
-        import torch
-        if self._ws is None or self._ws_bytes < need:
-            if self._ws is not None:
-                # the caching allocator tracks only the allocating stream: keep the old buffer from being
-                # handed out again before work already enqueued on the other streams that used it is done
-                for st in self._ws_streams:
-                    self._ws.record_stream(torch.cuda.ExternalStream(st, device=self.device))
-                if self._ws_captured:
-                    self._ws_kept.append(self._ws)
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-            self._ws_bytes = max(need, 256)
-            self._ws_streams = []
-            self._ws_captured = False
-        return self._ws, self._ws_bytes
-
-    def _pool(self, stream):
-        """The context in which memory for work on ``stream`` (None, a torch stream or a raw handle) is allocated: a
-        block of the current stream's pool may still be in use by work pending there."""
-        import torch
-        if stream is None:
-            return contextlib.nullcontext()
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int)
-                                 else stream)
-
-    def _output(self, T: int, stream):
-        """[T, H] for the kernels on ``stream`` to write; once dropped, reused only behind the current stream's work at
-        that time, which may read it."""
-        import torch
-        with self._pool(stream):
-            y = torch.empty((T, self.shapes.H), dtype=torch.bfloat16, device=self.device)
-        if stream is not None:
-            y.record_stream(torch.cuda.current_stream(self.device))
-        return y
-
-    def _note_stream(self, stream):
-        """Remember what the workspace is used by: the stream (None, a torch stream or a raw handle), a capture."""
-        import torch
-        st = moe._stream(stream)
-        if st not in self._ws_streams:
-            self._ws_streams.append(st)
-        if not self._ws_captured:
-            with self._pool(stream):
-                self._ws_captured = torch.cuda.is_current_stream_capturing()
-
-    def _check_tensors(self, *tensors):
-        """Refuses, before anything is enqueued, tensors given as (name, tensor, shapes, dtypes) that the kernels would
-        misread or write astray: another shape, type, order or device than the layer's, which is the current one."""
-        at = self.w["w_router"].get_device()
-        for name, t, shapes, dtypes in tensors:
-            if t.dtype in dtypes and t.shape in shapes and t.is_contiguous() and t.get_device() == at >= 0:
-                continue
-            if t.dtype not in dtypes:
-                raise ValueError(f"{name} is {t.dtype}; expected {' or '.join(map(str, dtypes))}")
-            if t.shape not in shapes:
-                raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {' or '.join(map(str, shapes))}")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            raise ValueError(f"{name} is on {t.device}, the layer on {self.w['w_router'].device}")
-        if at != moe._device():
-            raise ValueError(f"the layer is on GPU {at}; the current one is {moe._device()}")
 
     def forward(self, x, y=None, stream=None):
         """y = layer(x); x is a [T, H] bfloat16 device tensor."""
@@ -467,3 +484,132 @@ class PrefillRunner:
             self.close()
         except Exception:
             pass
+
+
+class DeviceAttention(_Resident):
+    """The attention half of a block on one GPU: the q, k and v projections as one product, norms of the heads, rotary
+    positions, a paged cache, attention over it, and the output projection.
+
+    ``weights`` (bf16 bit patterns, numpy uint16, as DeviceLayer takes them): ``w_qkv`` [(Hq + 2 Hkv) D, H], ``w_o``
+    [H, Hq D]; optional ``q_norm`` and ``k_norm`` [D], ``b_qkv`` and ``b_o`` (float32).  ``cache``: "bf16", "i8" or
+    "e4m3"; the cache has ``n_pages`` pages of ``page`` tokens and is the object's own.  ``freq`` and ``mscale`` are
+    moe_rope_frequencies' (None: no rotation), ``pairs`` how they pair a head's elements; ``w_add`` is added to the
+    heads' norm weights.
+
+    A step's tokens are described by device tensors of int32: ``pos`` and ``slots`` [T], ``pages`` [S, pages a
+    sequence], ``q_start`` [S + 1], ``kv_len`` [S] (see moe_cache_write and moe_attention).  They are read when the
+    kernels run, so a captured step is replayed over new ones.  Calls of one object share its workspace and its cache;
+    the rules of DeviceLayer hold.
+    """
+
+    CACHES = ("bf16", "i8", "e4m3")
+
+    def __init__(self, weights: Dict[str, np.ndarray], Hq: int, Hkv: int, D: int, n_pages: int, page: int = 64,
+                 cache: str = "bf16", freq=None, mscale: float = 1.0, pairs: int = moe.ROPE_HALF, window: int = 0,
+                 scale: Optional[float] = None, w_add: float = 0.0, eps: float = 1e-6, device="cuda:0"):
+        import torch
+        if cache not in self.CACHES:
+            raise ValueError(f"cache is {cache!r}; expected one of {', '.join(self.CACHES)}")
+        self.device = torch.device(device)
+        self.w = {key: to_device_bf16(weights.get(key), self.device) for key in ("w_qkv", "w_o", "q_norm", "k_norm")}
+        self.b = {key: None if weights.get(key) is None else
+                  torch.from_numpy(np.ascontiguousarray(weights[key], np.float32)).to(self.device)
+                  for key in ("b_qkv", "b_o")}
+        H = self.w["w_qkv"].shape[1]
+        for key, t, shape in (("w_qkv", self.w["w_qkv"], ((Hq + 2 * Hkv) * D, H)), ("w_o", self.w["w_o"], (H, Hq * D)),
+                              ("q_norm", self.w["q_norm"], (D,)), ("k_norm", self.w["k_norm"], (D,)),
+                              ("b_qkv", self.b["b_qkv"], ((Hq + 2 * Hkv) * D,)), ("b_o", self.b["b_o"], (H,))):
+            if t is not None and t.shape != shape:
+                raise ValueError(f"{key} has shape {tuple(t.shape)}; expected {shape}")
+        self.H, self.Hq, self.Hkv, self.D = H, Hq, Hkv, D
+        self.n_pages, self.page, self.window, self.scale = n_pages, page, window, scale
+        self.rot = 0 if freq is None else 2 * freq.numel()
+        self.freq = None if freq is None else freq.to(self.device)
+        self.mscale, self.pairs, self.w_add, self.eps = mscale, pairs, w_add, eps
+        dtype = {"bf16": torch.bfloat16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}[cache]
+        shape = (n_pages, Hkv, page, D)
+        self.k_cache, self.v_cache = (torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
+        self.k_scale, self.v_scale = ((None, None) if cache == "bf16" else
+                                      (torch.zeros(shape[:3], device=self.device) for _ in range(2)))
+        self._init_workspace()
+        with torch.cuda.device(self.device):
+            # the first forward may run on any stream
+            torch.cuda.current_stream().synchronize()
+
+    @property
+    def _home(self):
+        return self.w["w_qkv"]
+
+    @property
+    def _width(self):
+        return self.H
+
+    def _buffers(self, T: int, S: int, max_keys: int):
+        """(q, k, v columns of one product's rows, attention's output, its workspace), views of the workspace."""
+        import torch
+        qkv, o = T * (self.Hq + 2 * self.Hkv) * self.D * 2, T * self.Hq * self.D * 2
+        part = moe.moe_attention_workspace_size(T, S, self.Hq, self.Hkv, self.D, max_keys)
+        up = [-(-n // 256) * 256 for n in (qkv, o, part)]
+        ws, _ = self._reserve(sum(up))
+        rows = ws[:qkv].view(torch.bfloat16).view(T, -1)
+        nq, nk = self.Hq * self.D, self.Hkv * self.D
+        return (rows, rows[:, :nq], rows[:, nq:nq + nk], rows[:, nq + nk:],
+                ws[up[0]:up[0] + o].view(torch.bfloat16).view(T, nq),
+                ws[up[0] + up[1]:up[0] + up[1] + part] if part else None)
+
+    def _check_step(self, T, pos, slots, pages, q_start, kv_len):
+        import torch
+        i32 = (torch.int32,)
+        S = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        m = pages.shape[-1]
+        given = [("slots", slots, ((T,),), i32), ("pages", pages, ((S, m),), i32), ("q_start", q_start, ((S + 1,),), i32),
+                 ("kv_len", kv_len, ((S,),), i32)]
+        if self.rot or pos is not None:
+            given.append(("pos", pos, ((T,),), i32))
+        self._check_tensors(*given)
+        return S, m
+
+    def forward(self, x, pos, slots, pages, q_start, kv_len, add=None, out=None, stream=None):
+        """[T, H]: attention of the rows x [T, H] (bf16, normed), whose keys and values go to the cache first, through
+        the output projection, plus ``add`` [T, H].  Rows outside all sequences of q_start are projections of whatever
+        the workspace held."""
+        import torch
+        T, bf = x.shape[0], (torch.bfloat16,)
+        rows = ((T, self.H),)
+        self._check_tensors(*((n, t, rows, bf) for n, t in (("x", x), ("add", add), ("out", out)) if t is not None))
+        S, m = self._check_step(T, pos, slots, pages, q_start, kv_len)
+        if out is None:
+            out = self._output(T, stream)
+        if T == 0:
+            return out
+        with self._pool(stream):
+            qkv, q, k, v, o, part = self._buffers(T, S, m * self.page)
+        self._note_stream(stream)
+        w = self.w
+        moe.moe_gemm(x, w["w_qkv"], self.b["b_qkv"], None, T, qkv.shape[1], self.H, qkv, stream=stream)
+        moe.moe_cache_write(q, w["q_norm"], q, k, w["k_norm"], v, pos if self.rot else None, self.freq, slots, T, self.Hq,
+                            self.Hkv, self.D, self.rot, self.pairs, self.k_cache, self.v_cache, self.k_scale,
+                            self.v_scale, self.n_pages, self.page, self.mscale, self.w_add, self.eps, stream)
+        moe.moe_attention(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, pages, q_start, kv_len, T, S,
+                          self.Hq, self.Hkv, self.D, self.n_pages, self.page, m, o, part, self.scale, self.window,
+                          stream=stream)
+        moe.moe_gemm(o, w["w_o"], self.b["b_o"], add, T, self.H, self.Hq * self.D, out, stream=stream)
+        return out
+
+    def forward_block(self, r, y, w_pre, pos, slots, pages, q_start, kv_len, w_post=None, gate=None,
+                      r_scale: float = 1.0, y_scale: float = 1.0, w_add: float = 0.0, eps: float = 1e-6, out=None,
+                      stream=None):
+        """Attention as a block of a residual stream, as DeviceLayer.forward_block: r (in place) takes the previous
+        block's output y through moe_block_norm, and attention runs on the normed rows."""
+        import torch
+        bf = torch.bfloat16
+        T = r.shape[0]
+        rows, one = ((T, self.H),), ((self.H,), (1, self.H))
+        given = (("r", r, rows, (bf, torch.float32)), ("y", y, rows, (bf,)), ("w_pre", w_pre, one, (bf,)),
+                 ("w_post", w_post, one, (bf,)), ("gate", gate, one + rows, (bf,)), ("out", out, rows, (bf,)))
+        self._check_tensors(*(g for g in given if g[1] is not None))
+        self._check_step(T, pos, slots, pages, q_start, kv_len)
+        with self._pool(stream):
+            x = torch.empty((T, self.H), dtype=bf, device=self.device)
+        moe.moe_block_norm(r, y, w_post, gate, w_pre, T, self.H, r, x, None, None, r_scale, y_scale, w_add, eps, stream)
+        return self.forward(x, pos, slots, pages, q_start, kv_len, out=out, stream=stream)
