@@ -495,7 +495,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         for (int e = 0; e < 16; ++e) top = fmaxf(top, x[b][e]);
       top = halves_max(top) * scale;
       if (__any(top > mx + kSlack)) {
-        const float to = fmaxf(mx, top);
+        const float to = top > mx + kSlack ? top : mx;  // a row's own need: its bits do not depend on its neighbours'
         const float f = exp2_fast(mx - (to == kNegInf ? 0.0f : to));
         mx = to;
         l *= f;
@@ -841,8 +841,11 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
   const int unit = few ? (D == 64 ? 256 : 128) : 64;
   const int64_t tiles = T * G / p.rows + S;  // or fewer
   const int64_t units = (max_keys + 63 + unit - 1) / unit;
-  p.min_units = few ? 1 : 4;
-  p.stream = few ? max_keys > 2 * unit : items_of(128) < 384 && units > 2 * p.min_units;
+  // Row tiles of 128 to share out below 256 of them, for long contexts only: what is shared has to be joined, and the
+  // shares count masked keys.  Shared / not, us: prompts of 512 and 1024 (128 and 256 tiles) 30 / 19 and 53 / 31; 4 chunks
+  // of 128 behind 1024 (128 tiles) 46 / 33, 2 of 256 behind 4096 75 / 103, one of 512 behind 8192 at D 64 76 / 165.
+  p.min_units = few ? 1 : 8;
+  p.stream = few ? max_keys > 2 * unit : items_of(128) < 256 && units > 32;
   const int64_t all = tiles * Hkv * (p.stream ? (units + p.min_units - 1) / p.min_units : 1);
   const int64_t most = D == 256 ? 256 : 512;
   p.grid = (int)(p.stream && all > most ? most : all);

@@ -16,7 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;  // heads whose loads a lane has in flight
+constexpr int kUnits = 2;  // heads whose loads a lane has in flight
 
 template <int CTRL, int BANKS = 0xf>
 __device__ __forceinline__ float dpp(float old, float v) {
@@ -101,18 +101,31 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int per_tok
   const bool lower = c * 8 < half;  // (unless kInside or kOdd) the chunk holds pairs' first elements
   if (p.rot > 0) {
     const double pos = (double)p.pos[t];
+    auto angle = [&](int pair, float& cs, float& sn) {
+      const double turns = pos * p.freq[pair];
+      sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
+      cs *= p.mscale, sn *= p.mscale;
+    };
+    if constexpr (PAIRS == kWhole) {
+      // the lanes LPH / 2 apart hold the same pairs: each works out four of the eight
 #pragma unroll
-    for (int e = 0; e < NC; ++e) {
-      const int i = PAIRS == kInside ? c * 4 + e : c * 8 + e;
-      const int pair = PAIRS == kInside || i < half ? i : i - half;
-      co[e] = 1.0f, si[e] = 0.0f;
-      if (PAIRS == kInside ? i < half : i < p.rot) {
-        const double turns = pos * p.freq[pair];
-        float sn, cs;
-        sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-        co[e] = cs * p.mscale, si[e] = sn * p.mscale;
-        // the second element of a pair takes the first with the other sign
-        if (PAIRS != kInside && i < half) si[e] = -si[e];
+      for (int e = 0; e < 4; ++e) {
+        float cs, sn;
+        angle((c & (LPH / 2 - 1)) * 8 + (lower ? e : e + 4), cs, sn);
+        const float oc = other_half<LPH>(cs, c), os = other_half<LPH>(sn, c);
+        co[e] = lower ? cs : oc, si[e] = lower ? -sn : os;
+        co[e + 4] = lower ? oc : cs, si[e + 4] = lower ? -os : sn;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < NC; ++e) {
+        const int i = PAIRS == kInside ? c * 4 + e : c * 8 + e;
+        co[e] = 1.0f, si[e] = 0.0f;
+        if (PAIRS == kInside ? i < half : i < p.rot) {
+          angle(PAIRS == kInside || i < half ? i : i - half, co[e], si[e]);
+          // the second element of a pair takes the first with the other sign
+          if (PAIRS != kInside && i < half) si[e] = -si[e];
+        }
       }
     }
   }
