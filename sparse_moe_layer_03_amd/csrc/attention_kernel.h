@@ -68,7 +68,11 @@ struct Cfg {
   // Page numbers a wave looks up per tile: of every load of whole rows, or of every 16 keys.  The 64 lanes of such a load
   // read rows that begin at a multiple of, and are at most, 16, so they lie in one page whatever its size.
   static constexpr int NP = KREG ? KT / 16 : NL;
-  static constexpr int LDS = WK * NB * STAGE + (WK > 1 ? WK * 64 * 4 : 0);
+  // q in LDS where it, O and the loads in flight would not fit the registers (spills wait behind those loads: 64 decode
+  // requests at D 256 ... us with q in registers)
+  static constexpr bool QLDS = KREG && D == 256 && !QUANT;
+  static constexpr int SUMS = WK * NB * STAGE, QS = SUMS + (WK > 1 ? WK * 64 * 4 : 0);  // offsets in LDS
+  static constexpr int LDS = QS + (QLDS ? 32 * KROW : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
   static_assert(WK == 1 || WR == 1, "");
@@ -276,8 +280,19 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     const int pos = live ? pos0 + tok : -1;
     const int vis0 = p.window > 0 ? max(pos - p.window + 1, 0) : 0, vis_n = max(pos - vis0 + 1, 0);
 
-    bf16x8 qf[C::NQ];
-    {
+    bf16x8 qf[C::QLDS ? 1 : C::NQ];
+    const lds_bytes ql_at = smem + C::QS + ql * C::KROW + 16 * hh;
+    if constexpr (C::QLDS) {
+      // the waves' rows are the same: each brings its share
+      const uint16_t* qp = p.q + (q.q0 + tok) * p.q_ld + (int64_t)head * D + 8 * hh;
+#pragma unroll
+      for (int i = 0; i < C::NQ / WK; ++i) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (live) v = *reinterpret_cast<const u32x4*>(qp + 16 * (wk * (C::NQ / WK) + i));
+        *lds_as<u32x4>(ql_at + 32 * (wk * (C::NQ / WK) + i)) = v;
+      }
+      __syncthreads();
+    } else {
       // a K load of 16 codes is two steps' operand
       constexpr bool PAIRS = C::KREG && C::QUANT;
       const uint16_t* qp = p.q + (q.q0 + tok) * p.q_ld + (int64_t)head * D + (PAIRS ? 16 : 8) * hh;
@@ -454,7 +469,12 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
             x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, lo), qf[2 * i], x[b], 0, 0, 0);
             x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi), qf[2 * i + 1], x[b], 0, 0, 0);
           } else {
-            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k), qf[i], x[b], 0, 0, 0);
+            bf16x8 f;
+            if constexpr (C::QLDS)
+              f = *lds_as<bf16x8>(ql_at + 32 * i);
+            else
+              f = qf[i];
+            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k), f, x[b], 0, 0, 0);
           }
         }
         if (bad >> 2 * b & 3) {  // keys 32 b .. + 15 or + 16 .. + 31 have no page
@@ -664,29 +684,29 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         step(nt - 1, std::true_type());
         if (!second) sync();
       } else {
-      auto step = [&](int j, auto last) {
-        const int buf = j & 1;
-        if (wave_live) {
-          maximum(key_of(j), buf, x);
-          weights(buf, x, hi, lo);
-          if constexpr (!decltype(last)::value) {
+        auto step = [&](int j, auto last) {
+          const int buf = j & 1;
+          if (wave_live) {
+            maximum(key_of(j), buf, x);
+            weights(buf, x, hi, lo);
+            if constexpr (!decltype(last)::value) {
 #pragma unroll
-            for (int b = 0; b < C::KB; ++b) x[b] = f32x16{};
-            scores(buf ^ 1, x);
+              for (int b = 0; b < C::KB; ++b) x[b] = f32x16{};
+              scores(buf ^ 1, x);
+            }
+            product(buf, hi, lo);
           }
-          product(buf, hi, lo);
-        }
-        if constexpr (!decltype(last)::value) {
-          if (j + 2 < nt) store_k(j + 2, buf, bad);
-          store_v(j + 1, buf ^ 1, vbad);
-          if constexpr (C::QUANT) store_scales(buf ^ 1);
-          if (j + 2 < nt) to_v(), next_v(j + 2);
-          if (j + 3 < nt) next_k(j + 3);
-          sync();
-        }
-      };
-      for (int j = 0; j < nt - 1; ++j) step(j, std::false_type());
-      step(nt - 1, std::true_type());
+          if constexpr (!decltype(last)::value) {
+            if (j + 2 < nt) store_k(j + 2, buf, bad);
+            store_v(j + 1, buf ^ 1, vbad);
+            if constexpr (C::QUANT) store_scales(buf ^ 1);
+            if (j + 2 < nt) to_v(), next_v(j + 2);
+            if (j + 3 < nt) next_k(j + 3);
+            sync();
+          }
+        };
+        for (int j = 0; j < nt - 1; ++j) step(j, std::false_type());
+        step(nt - 1, std::true_type());
       }
     }
     l = halves_sum(l);
@@ -729,6 +749,10 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
             for (int e = 0; e < E; ++e) ov[e] = ov[e] * f + wv * cached<C::CT>(p.v_cache, at * D + lane + 64 * e);
           }
+          bool lost = true;  // all of it NaN: so it stays
+#pragma unroll
+          for (int e = 0; e < E; ++e) lost = lost && ov[e] != ov[e];
+          if (__all(lost)) break;
         }
 #pragma unroll
         for (int d = 0; d < C::DB; ++d)
@@ -781,7 +805,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       if (WR > 1 && STREAM) __syncthreads();  // before the next item's first tile
     } else {
       // the waves' results of the same rows joined: each adds its share of the elements of all
-      MOE_LDS f32x2* ml = lds_as<f32x2>(smem + WK * C::NB * C::STAGE) + anew(ql);  // [WK][32]
+      MOE_LDS f32x2* ml = lds_as<f32x2>(smem + C::SUMS) + anew(ql);  // [WK][32]
       MOE_LDS float* mine = lds_as<float>(group) + anew(lane);                    // [16 DB][64]
       if (hh == 0) ml[wk * 32] = f32x2{mx, l};
       __syncthreads();
