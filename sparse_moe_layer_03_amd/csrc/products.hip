@@ -189,13 +189,14 @@ __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRow
 
 // ---------------------------------------------------------------------------------------------------------------
 // Few rows (dense products): a workgroup owns 16 columns and reads their weights once, straight into
-// registers.  Its four waves take every fourth 128-byte line of the rows (two 16 x 16 matrix instructions deep), U
-// lines at a time, and add their partial sums through LDS.  One row by 2048 x 4096 takes 3.2 us, a launch and one round
-// of loads; the bytes alone would take 1.8.
+// registers.  Its W waves take every W-th 128-byte line of the rows (two 16 x 16 matrix instructions deep), U lines at
+// a time, and add their partial sums through LDS.  The loads in flight bound it: an 8-bit row by 2048 x 4096 takes 3.2
+// us with four waves, a launch and one round of loads (the bytes alone would take 1.8).  A bf16 row's lines are twice
+// as many: by 2048 x 4096, with weights that lie in no cache, eight waves take 8.1 us and four 10.0, by 512 x 8192 12.4
+// and 16.1, by 8192 x 4096 17.4 and 17.1 (3.9 TB/s); 40 rows by 2048 x 512 5.2 and 4.6.
 
-template <bool I8, bool F32, int EPI, int MT, int U>
-__global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
-  constexpr int W = 4;
+template <bool I8, bool F32, int EPI, int MT, int U, int W>
+__global__ __launch_bounds__(64 * W) void skinny_kernel(ProductArgs p) {
   typedef typename Acc<I8>::t16 acc_t;
   __shared__ acc_t part[W][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -233,7 +234,9 @@ __global__ __launch_bounds__(256) void skinny_kernel(ProductArgs p) {
   __syncthreads();
   // wave m adds and stores row block m: lane l holds, of row l & 15, columns 4 (l >> 4) + i
   for (int m = wave; m < MT; m += W) {
-    const acc_t s = (part[0][m][lane] + part[1][m][lane]) + (part[2][m][lane] + part[3][m][lane]);
+    acc_t s = (part[0][m][lane] + part[1][m][lane]) + (part[2][m][lane] + part[3][m][lane]);
+    if constexpr (W == 8)
+      s += (part[4][m][lane] + part[5][m][lane]) + (part[6][m][lane] + part[7][m][lane]);
     const int id = 16 * m + (lane & 15), n = n0 + 4 * (lane >> 4);
     if (id >= p.P || n >= p.N) continue;
     const size_t at = (size_t)id * p.N + n;
@@ -683,12 +686,13 @@ hipError_t dense_launch(const ProductArgs& p, hipStream_t st) {
   // 64 rows 7.3 against 6.5, 33 x 4096 x 4096 11.1 against 9.5 (every workgroup reads all rows of A, and its loads
   // come in batches).  256 workgroups fill the CUs.
   const unsigned blocks = (unsigned)((p.N + 15) / 16);
+  constexpr int W = I8 ? 4 : 8;
   if (p.P <= 16) {
-    skinny_kernel<I8, F32, EPI, 1, 4><<<blocks, 256, 0, st>>>(p);
+    skinny_kernel<I8, F32, EPI, 1, 4, W><<<blocks, 64 * W, 0, st>>>(p);
     return hipGetLastError();
   }
   if (p.P <= 64 && p.Kb <= 2048 && p.P * p.Kb <= 48 * 2048 && blocks <= 256) {
-    skinny_kernel<I8, F32, EPI, 4, 2><<<blocks, 256, 0, st>>>(p);
+    skinny_kernel<I8, F32, EPI, 4, 2, W><<<blocks, 64 * W, 0, st>>>(p);
     return hipGetLastError();
   }
   return tiled_launch<I8, F32, EPI, false>(p, st);
