@@ -4,17 +4,33 @@
 // G query heads, so that all of them read the key head's cache once.  Per 32 rows and 32 keys
 //   S^T = K Q^T      lane l holds query row l & 31, keys 8 g + 4 (l >> 5) + i in register 4 g + i
 //   O^T = V^T P^T    the same lanes hold the row's P, which the instruction takes as they are: its 16 keys a step are
-//                    numbered 4 h + i and 8 + 4 h + i of lane half h, and V^T is read from LDS in that order, transposed
-//                    by the LDS read itself
+//                    numbered 4 h + i and 8 + 4 h + i of lane half h, and V^T is read from LDS in that order,
+//                    transposed by the LDS read itself
 // so neither S nor P leaves its lane.  Softmax is the online form in base 2: running maximum m, sum l and O in fp32,
 // rescaled when a tile raises m by more than 2^kSlack.  P is rounded to bf16 for its product, an error of the size of
-// the output's own rounding (half a step, 2^-8 of each weight); where few rows leave the matrix cores idle the rest of it
-// goes in as a second bf16 term (2^-16).  l sums the unrounded values.
+// the output's own rounding (half a step, 2^-8 of each weight); where few rows leave the matrix cores idle the rest of
+// it goes in as a second bf16 term (2^-16).  l sums the unrounded values.
 //
 // A masked key has P = 0, which does not undo an Inf or NaN in its V: rows behind the range of keys that the tile's
 // rows can see are zeroed on the way into LDS; a key inside it that only some rows see (later tokens, the window's
 // edge) could still poison the others, which shows as a non-finite O.  Rows with one are computed again, key by key
-// over the visible ones alone, at the end (`careful`).
+// over the visible ones alone, at the end.
+//
+// Three shapes.  Up to 32 rows a sequence (decoding, drafts): 32 rows, four waves that deal the keys out between them,
+// K straight into the operand registers; the cache's bytes bound it.  64 requests of up to 8192 keys (4 heads of 128 in
+// bf16, 537 MB) take 114 us, 4.7 TB/s, and 4.7 us to join, where the loads alone take 116 in all.  More rows: 128 rows
+// in four waves that share tiles of 64 keys; with 512 such items of D 128 in bf16 256 rows in eight waves.  Bound
+// between the matrix and the vector instructions: a prompt of 8192 tokens, 32 heads over 4, takes 531 us, 1034 TFLOP/s
+// of the 1487 that a large product reaches; of a wave's cycles the matrix instructions take 45%, the vector ones 40%
+// (exponentials, maxima, rounding), LDS 28% without bank conflicts, and a third are waits.  At D 64 the exponentials
+// weigh twice as much: 825 TFLOP/s.  Wide / narrow tiles, us: a prompt of 4096 148 / 163, two chunks of 1024 behind
+// 8192 283 / 316, but one of 2048 (256 wide items) 68 / 59; at D 64, where three narrow workgroups fit a CU, a prompt
+// of 8192 386 / 333.
+//
+// Measured and not taken, in us: two row blocks a wave (prefill 838 against 534, spills; D 64 312 against 328, but a
+// window of 1024 91 against 80); tiles two deep in flight for 8-bit caches (no change); loads past the caches (decode
+// 136 against 122); 256 workgroups instead of 512 at D up to 128 (decode 126 against 122, drafts 54 against 35); a
+// wave's priority raised around its products, and the compiler's schedule groups (no change).
 #pragma once
 
 #include <atomic>
@@ -65,11 +81,11 @@ struct Cfg {
   static constexpr bool KREG = WR == 1;  // K goes from memory into the operand registers
   static constexpr int KTILE = KREG ? 0 : KT * KROW;
   static constexpr int STAGE = (KTILE + KT * VROW > 32 * D * 4 || WK == 1 ? KTILE + KT * VROW : 32 * D * 4) + SCALES;
-  // Page numbers a wave looks up per tile: of every load of whole rows, or of every 16 keys.  The 64 lanes of such a load
-  // read rows that begin at a multiple of, and are at most, 16, so they lie in one page whatever its size.
+  // Page numbers a wave looks up per tile: of every load of whole rows, or of every 16 keys.  The 64 lanes of such a
+  // load read rows that begin at a multiple of, and are at most, 16, so they lie in one page whatever its size.
   static constexpr int NP = KREG ? KT / 16 : NL;
   // q in LDS where it, O and the loads in flight would not fit the registers (spills wait behind those loads: 64 decode
-  // requests at D 256 ... us with q in registers)
+  // requests at D 256 134 us, 151 with q in registers)
   static constexpr bool QLDS = KREG && D == 256 && !QUANT;
   static constexpr int SUMS = WK * NB * STAGE, QS = SUMS + (WK > 1 ? WK * 64 * 4 : 0);  // offsets in LDS
   static constexpr int LDS = QS + (QLDS ? 32 * KROW : 0);
@@ -142,7 +158,8 @@ __device__ __forceinline__ int find(int S, int lane, int64_t at, W weight, int64
   }
   return S;
 }
-// Share `index` of `shares` equal ones (none below `least`) of all weights: its begin and end, and as `find` for its begin.
+// Share `index` of `shares` equal ones (none below `least`) of all weights: its begin and end, and as `find` for its
+// begin.
 template <class W>
 __device__ __forceinline__ int find_share(int S, int lane, int index, int shares, int least, W weight, int64_t& share,
                                           int64_t& begin, int64_t& end, int64_t& before) {
@@ -202,8 +219,8 @@ __device__ __forceinline__ float cached(const void* p, int64_t i) {
   return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p)[i], 0);
 }
 
-// Partial results in the workspace: a Part per workgroup, then slots of R rows of O (unscaled, fp32) and R pairs (m, l).
-// Part w: the item that begins in workgroup w's share and ends behind it.
+// Partial results in the workspace: a Part per workgroup, then slots of R rows of O (unscaled, fp32) and R pairs
+// (m, l).  Part w: the item that begins in workgroup w's share and ends behind it.
 struct Part {
   int n;     // workgroups that hold a part of it, w the first; 0: there is no such item
   int rows;  // of the item
@@ -217,8 +234,8 @@ __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
 }
 
 // One workgroup computes one (sequence, key head, row tile), or (STREAM) its equal share of all units of work, which
-// may begin and end inside such an item: what is not a whole item goes to the workspace, slot 2 w for the end of an item
-// and 2 w + 1 for a beginning, and combine_kernel joins it.
+// may begin and end inside such an item: what is not a whole item goes to the workspace, slot 2 w for the end of an
+// item and 2 w + 1 for a beginning, and combine_kernel joins it.
 template <class C, bool STREAM>
 __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, lds_bytes smem) {
   constexpr int D = C::D, KT = C::KT, WR = C::WR, WK = C::WK;
@@ -319,7 +336,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     unsigned bad = 0;    // bit i: there is no such page
     int page[C::NP];     // of the next tile: a scalar load's latency ahead
     int64_t off[C::NP];  // of the tile at hand: where its rows begin in the cache, in bytes
-    const uint32_t page_bytes = (uint32_t)p.Hkv * C::ROWB << p.page_shift, head_bytes = (uint32_t)h * C::ROWB << p.page_shift;
+    const uint32_t page_bytes = (uint32_t)p.Hkv * C::ROWB << p.page_shift;
+    const uint32_t head_bytes = (uint32_t)h * C::ROWB << p.page_shift;
     auto look_up = [&](int j) {
       const int k0 = key_of(j);
 #pragma unroll
@@ -337,8 +355,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       }
       if (j + 1 < nt) look_up(j + 1);
     };
-    // Scales: a wave alone has the pages of all keys at hand; where more share a tile each lane looks up its own, a tile
-    // ahead.
+    // Scales: a wave alone has the pages of all keys at hand; where more share a tile each lane looks up its own, a
+    // tile ahead.
     int s_page[C::NS];
     auto scale_key = [&](int j, int i) { return key_of(j) + (i * C::GT + gt) % KT; };
     auto look_up_scales = [&](int j) {
@@ -360,7 +378,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           if (x < 2 * KT && key >= kb && key < ke && !(bad >> g & 1))
             rs[i] = (x < KT ? p.k_scale : p.v_scale)[row / C::ROWB + (x & 15)];
         } else if (x < 2 * KT && key >= kb && key < ke && (unsigned)s_page[i] < (unsigned)p.n_pages) {
-          rs[i] = (x < KT ? p.k_scale : p.v_scale)[(((int64_t)s_page[i] * p.Hkv + h) << p.page_shift) + (key & page_mask)];
+          const int64_t at = (((int64_t)s_page[i] * p.Hkv + h) << p.page_shift) + (key & page_mask);
+          rs[i] = (x < KT ? p.k_scale : p.v_scale)[at];
         }
       }
       if (j + 1 < nt) look_up_scales(j + 1);
@@ -382,7 +401,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     auto issue_k = [&]() {
 #pragma unroll
       for (int b = 0; b < C::KB; ++b) {
-        const char* at = static_cast<const char*>(p.k_cache) + (ql < 16 ? off[2 * b % C::NP] : off[(2 * b + 1) % C::NP]);
+        const char* at = static_cast<const char*>(p.k_cache);
+        at += ql < 16 ? off[2 * b % C::NP] : off[(2 * b + 1) % C::NP];
         at += (ql & 15) * C::ROWB + 16 * hh;
 #pragma unroll
         for (int i = 0; i < C::CPR / 2; ++i) rk[b * (C::CPR / 2) + i] = *reinterpret_cast<const u32x4*>(at + 32 * i);
@@ -390,8 +410,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     };
     // this lane's place of load i
     const int c_lane = (wr * 64 + lane) % C::CPR, r_lane = (wr * 64 + lane) / C::CPR;
-    // to LDS as bf16.  Rows outside the tile's range of keys become zeros; without a page (none: its bits) K becomes NaN,
-    // and with it the scores of the rows that see it, V zeros.
+    // to LDS as bf16.  Rows outside the tile's range of keys become zeros; without a page (none: its bits) K becomes
+    // NaN, and with it the scores of the rows that see it, V zeros.
     auto page_no = [&](int i) { return KREG ? i * 64 / C::CPR / 16 : i; };  // of load i
     auto store_rows = [&](u32x4* from, int j, lds_bytes to, int row_bytes, unsigned none, bool is_k) {
       const int k0 = key_of(j);
@@ -431,7 +451,9 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       }
     };
     auto buf_v = [&](int buf) { return group + buf * C::STAGE + C::KTILE; };
-    auto store_k = [&](int j, int buf, unsigned none) { store_rows(rk, j, group + buf * C::STAGE, C::KROW, none, true); };
+    auto store_k = [&](int j, int buf, unsigned none) {
+      store_rows(rk, j, group + buf * C::STAGE, C::KROW, none, true);
+    };
     auto store_v = [&](int j, int buf, unsigned none) { store_rows(rv, j, buf_v(buf), C::VROW, none, false); };
     auto store_scales = [&](int buf) {
       MOE_LDS float* ls = lds_as<float>(buf_v(buf) + KT * C::VROW);
@@ -467,7 +489,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
             u32x4 lo, hi;
             widen<C::CT>(k, lo, hi);
             x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, lo), qf[2 * i], x[b], 0, 0, 0);
-            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi), qf[2 * i + 1], x[b], 0, 0, 0);
+            x[b] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, hi), qf[2 * i + 1], x[b], 0, 0, 0);
           } else {
             bf16x8 f;
             if constexpr (C::QLDS)
@@ -788,7 +811,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       if (to_slot)
         *reinterpret_cast<float2*>(slot + (size_t)C::R * D + 2 * srow) = make_float2(sm, sl);
       else if (live && p.lse)
-        p.lse[(int64_t)(q.q0 + tok) * p.Hq + head] = sl > 0.0f || sl != sl ? (sm + log2f(sl)) * 0.6931471805599453f : kNegInf;
+        p.lse[(int64_t)(q.q0 + tok) * p.Hq + head] =
+            sl > 0.0f || sl != sl ? (sm + log2f(sl)) * 0.6931471805599453f : kNegInf;
     };
     if constexpr (WK == 1) {
       const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -866,8 +890,9 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
   const int64_t tiles = T * G / p.rows + S;  // or fewer
   const int64_t units = (max_keys + 63 + unit - 1) / unit;
   // Row tiles of 128 to share out below 256 of them, for long contexts only: what is shared has to be joined, and the
-  // shares count masked keys.  Shared / not, us: prompts of 512 and 1024 (128 and 256 tiles) 30 / 19 and 53 / 31; 4 chunks
-  // of 128 behind 1024 (128 tiles) 46 / 33, 2 of 256 behind 4096 75 / 103, one of 512 behind 8192 at D 64 76 / 165.
+  // shares count masked keys.  Shared / not, us: prompts of 512 and 1024 (128 and 256 tiles) 30 / 19 and 53 / 31; 4
+  // chunks of 128 behind 1024 (128 tiles) 46 / 33, 2 of 256 behind 4096 75 / 103, one of 512 behind 8192 at D 64
+  // 76 / 165.
   p.min_units = few ? 1 : 8;
   p.stream = few ? max_keys > 2 * unit : items_of(128) < 256 && units > 32;
   const int64_t all = tiles * Hkv * (p.stream ? (units + p.min_units - 1) / p.min_units : 1);
@@ -876,9 +901,10 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
   return p;
 }
 
-// Joins the partial results of the items that more than one workgroup computed; grid.x as in the launch before.  A row is
-// a workgroup's, its parts dealt over the waves.  Two rounds of loads, the parts' maxima and sums and then their O, each
-// some 1 us: two contexts of 131072 (64 parts a row) ... us.
+// Joins the partial results of the items that more than one workgroup computed; grid.x as in the launch before.  Up to
+// FEW parts a row is a wave's, all its loads at once: 4.7 us for 64 requests, mostly the launch.  With more it is a
+// workgroup's, its parts dealt over the waves: two rounds of loads, the parts' maxima and sums and then their O, 7.7 us
+// for two contexts of 131072 (64 parts a row).
 template <class C>
 __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
   constexpr int E = C::D / 64, MOST = 512, FEW = 8;

@@ -2,8 +2,11 @@
 //
 // A head of D elements is a group of LPH lanes (8, 16 or 32) with a 16-byte chunk each.  A group works on heads of one
 // token, so that the sines and cosines of its chunk's pairs stay in registers; what lanes exchange (sums, maxima, the
-// other half of a rotated pair) goes by lane permutations.  No LDS and no barriers in the usual layouts.  (With a table
-// of a token's sines in LDS and sums by LDS permutes 8192 tokens of 16 + 16 heads took 54 us, ... now.)
+// other half of a rotated pair) goes by lane permutations.  No LDS and no barriers in the usual layouts.  The rows'
+// bytes bound it: 8192 tokens of 32 heads of 128 rotated, 134 MB, take 28.1 us (4.8 TB/s, a large copy 5.1).
+// Quantised, the vector instructions come on top: 8192 tokens with 16 heads of q and 8 each of k and v of 128, normed,
+// rotated and written in 8 bits, 117 MB, take 31.5 us (3.7 TB/s; 54 us with a table of a token's sines in LDS and sums
+// by LDS permutes).
 //
 // The angle of a pair i at position p is the fraction of p * freq[i] turns: the product is taken in 64 bits (in 32 a
 // position of 10^6 would leave the angle of the fastest pair 0.06 rad off), its sine and cosine in 32.
@@ -239,7 +242,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int per_tok
   }
 }
 
-// Rows of the cache by slot, 8 elements a thread.
+// Rows of the cache by slot, 8 elements a thread: a copy that gathers and widens, bound by its bytes (8192 tokens of
+// 8 + 8 heads of 128 from 8 bits to bf16, 50 MB, 12 us).
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheReadArgs p) {
   const int cph = p.D / 8, per = 2 * p.Hkv * cph;  // chunks of a head, of a slot's k and v rows
   const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;

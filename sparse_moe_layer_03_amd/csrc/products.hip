@@ -279,6 +279,8 @@ __global__ __launch_bounds__(64 * W) void skinny_kernel(ProductArgs p) {
 // plain read of 4 GiB reaches 6.8 (a direct-to-LDS load from L2 alone 127 GB/s per CU); the two-stage ring waits for
 // all loads at every step, and half of the experts fill a tile to less than a sixth.  Below a mean of about 64 rows per
 // expert the weights' stream is all: 32 tokens, some 77 experts, 55 us, 5.9 TB/s (a plain read of as much 5.9).
+// Dense bf16 8192 x 5120 x 2048 takes 159 us (1.08 PFLOP/s; a library's product 154 to 159), with bias, activation and
+// addend 197: 640 tiles of 256 x 256 are two and a half rounds over the CUs and cost three.
 //
 // Measured and not taken, dense / grouped in us against 128 / 390: four waves of 128 x 128 (spills) 143 / 457; loads
 // spread between the matrix instructions 134 / 425; the last sub-step's instructions behind the barrier 131 / 404;
@@ -691,6 +693,14 @@ hipError_t dense_launch(const ProductArgs& p, hipStream_t st) {
     skinny_kernel<I8, F32, EPI, 1, 4, W><<<blocks, 64 * W, 0, st>>>(p);
     return hipGetLastError();
   }
+  // bf16, 17 and 32 rows against the best tile, the weights from HBM: 2048 x 512 3.9 and 4.2 against 4.7 and 5.0,
+  // 2048 x 4096 12.1 and 14.7 against 16.3 and 17.2, 4096 x 2048 8.1 and 9.4 against 10.1 and 10.7; 5120 x 2048 12.4 and
+  // 15.5 against 10.3 and 10.8, 33 rows by 2048 x 4096 19.8 against 16.0
+  if constexpr (!I8)
+    if (p.P <= 32 && blocks <= 256) {
+      skinny_kernel<I8, F32, EPI, 2, 2, W><<<blocks, 64 * W, 0, st>>>(p);
+      return hipGetLastError();
+    }
   if (p.P <= 64 && p.Kb <= 2048 && p.P * p.Kb <= 48 * 2048 && blocks <= 256) {
     skinny_kernel<I8, F32, EPI, 4, 2, W><<<blocks, 64 * W, 0, st>>>(p);
     return hipGetLastError();
