@@ -12,7 +12,7 @@
 // position of 10^6 would leave the angle of the fastest pair 0.06 rad off), its sine and cosine in 32.
 //
 // Quantisation of a row as in moe_quantize_i8: a = max(max |x|, 2^-100), scale = a / top, code = x / scale rounded to
-// nearest, top = 127 or 448 (by reciprocals of 1 ulp); a row that holds Inf or NaN gets scale NaN and codes 0.
+// nearest, top = 127 or 448, as x times top / a in fp32; a row that holds Inf or NaN gets scale NaN and codes 0.
 #include "attend_internal.h"
 
 namespace moe {
@@ -219,8 +219,10 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int per_tok
         }));
         const bool bad = m >= 0x7f800000u;
         constexpr float top = TYPE == MOE_I8 ? 127.0f : 448.0f;
-        // (the reciprocal, 1 ulp, is taken of the scale: that of the largest floats is no normal one)
-        const float scale = fmaxf(__uint_as_float(m), kQuantTiny) * (1.0f / top), inv = __builtin_amdgcn_rcpf(scale);
+        const float a = fmaxf(__uint_as_float(m), kQuantTiny), scale = a * (1.0f / top);
+        // top / a in 32 bits: the scale's reciprocal (a's own is no normal number for the largest) and its residual.
+        // Quotients x / scale halfway between two codes, which rows of bf16 values have many of, are then found as such.
+        const float near = __builtin_amdgcn_rcpf(scale), inv = fmaf(fmaf(-near, a, top), near * (1.0f / top), near);
         u32x2 w = {0u, 0u};
         if constexpr (TYPE == MOE_I8) {
 #pragma unroll

@@ -217,6 +217,34 @@ def test_cache_extremes(torch, kind):
         assert bool((c[0, 1, :T] == top).all()) and bool((s[0, 1, :T] == torch.tensor(1.0) / top).all())
 
 
+@pytest.mark.parametrize("kind,j", [("i8", 1), ("e4m3", 1), ("e4m3", 3), ("e4m3", 5)])
+def test_cache_halves(torch, kind, j):
+    """Quotients halfway between two codes go to the even one.  Rows of bf16 values with a maximum of top * j: the code
+    of j * v is v rounded.  The factor top / (top * j) rounded to fp32 is off by 0, 1/3 and 2/5 of a unit at most for 1 /
+    1, 1 / 3 and 1 / 5, and v at most 31 / 16 of its power of two, so that a product is off by less than half a unit
+    and rounds to v itself."""
+    D, P = 64, 16
+    top = A.TOP[kind]
+    # i8: c + 1/2; e4m3: five significant bits, the last one set
+    v = torch.arange(31 if kind == "i8" else 15, dtype=torch.float32)
+    v = v + 0.5 if kind == "i8" else torch.cat([(17 + 2 * (v % 8)) * 2.0 ** e for e in (-5, 0, 3)])[:31]
+    rows = torch.zeros(4, D)
+    for i, e in enumerate((-9, 0, 1, 40)):
+        rows[i, :31], rows[i, 31:62] = v * j * 2.0 ** e, -v * j * 2.0 ** e
+        rows[i, 63] = top * j * 2.0 ** e
+    x = rows.to(torch.bfloat16)
+    assert torch.equal(x.float(), rows)
+    x = x.cuda()
+    kc, vc, ks, vs = new_cache(torch, kind, 1, 1, P, D)
+    slots = torch.arange(4, device="cuda").int()
+    moe.moe_cache_write(None, None, None, x, None, x, None, None, slots, 4, 0, 1, D, 0, 0, kc, vc, ks, vs, 1, P)
+    want = v.round() if kind == "i8" else v.to(torch.float8_e4m3fn).float()
+    for c in (kc, vc):
+        for i in range(4):
+            got = c[0, 0, i].float().cpu()
+            assert torch.equal(got[:31], want) and torch.equal(got[31:62], -want) and float(got[63]) == top
+
+
 # ------------------------------------------------------------------ attention
 class Case:
     """Sequences (new tokens, keys) over a cache of random pages; slots and table entries that no row sees hold
