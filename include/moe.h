@@ -593,9 +593,9 @@ int moe_cache_read(const void* k_cache, const void* v_cache, const float* k_scal
  *   them: its row i is at position p = kv_len[s] - n + i (n rows) and sees keys j with 0 <= j <= p and, with window
  *   > 0, j > p - window.  Key j lies in page pages[s * max_pages + j / P], place j % P.
  *     out = softmax_j(scale * q . k_j) v        per query head; head h reads key head h / (Hq / Hkv)
- *   q, out [T, Hq*D] bf16, rows q_ld, out_ld apart, not overlapping.  lse [T, Hq] fp32 or NULL: ln sum_j e^(score),
- *   for joining results over different keys.  Rows that see no key: out 0, lse -infinity.  Rows outside all sequences
- *   are left as they were.
+ *   q, out [T, Hq*D] bf16, rows q_ld, out_ld apart; out may be q (with equal strides), else they do not overlap.
+ *   lse [T, Hq] fp32 or NULL: ln sum_j e^(score), for joining results over different keys.  Rows that see no key:
+ *   out 0, lse -infinity.  Rows outside all sequences are left as they were.
  *   Keys that no row sees are not read into any sum, whatever their slots hold: entries of pages that hold visible
  *   keys must lie in [0, n_pages) (else the rows that see them are NaN), others may hold anything.  kv_len beyond
  *   max_pages * P counts as that; q_start is cut to [0, T].  All three are read on the device.

@@ -229,6 +229,7 @@ int moe_attention(const uint16_t* q, int64_t q_ld, const void* k_cache, const vo
   if (T == 0 || S == 0) return ok();
   if (!q || !k_cache || !v_cache || !pages || !q_start || !kv_len || !out)
     return fail(MOE_ERR_NULL, "%s: q, the caches, pages, q_start, kv_len and out are required", f);
+  if (q == out && q_ld != out_ld) return fail(MOE_ERR_SHAPE, "%s: in place q_ld and out_ld must be equal", f);
   if ((rc = check_scales(f, type, k_scale, v_scale)) || (rc = check_aligned(f, q, k_cache, v_cache, out))) return rc;
   for (const void* s : {(const void*)pages, (const void*)q_start, (const void*)kv_len, (const void*)lse,
                         (const void*)k_scale, (const void*)v_scale})

@@ -235,7 +235,8 @@ __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
 
 // One workgroup computes one (sequence, key head, row tile), or (STREAM) its equal share of all units of work, which
 // may begin and end inside such an item: what is not a whole item goes to the workspace, slot 2 w for the end of an
-// item and 2 w + 1 for a beginning, and combine_kernel joins it.
+// item and 2 w + 1 for a beginning, and combine_kernel joins it.  out may be q: this workgroup alone reads the q of a
+// whole item, before it writes there, and what was cut is written in the next launch.
 template <class C, bool STREAM>
 __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_units, lds_bytes smem) {
   constexpr int D = C::D, KT = C::KT, WR = C::WR, WK = C::WK;

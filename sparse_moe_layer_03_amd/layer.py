@@ -545,7 +545,8 @@ class DeviceAttention(_Resident):
         return self.H
 
     def _buffers(self, T: int, S: int, max_keys: int):
-        """(q, k, v columns of one product's rows, attention's output, its workspace), views of the workspace."""
+        """(q, k, v columns of one product's rows, rows of rotated q and then of attention's output, its workspace), views
+        of the workspace."""
         import torch
         qkv, o = T * (self.Hq + 2 * self.Hkv) * self.D * 2, T * self.Hq * self.D * 2
         part = moe.moe_attention_workspace_size(T, S, self.Hq, self.Hkv, self.D, max_keys)
@@ -571,8 +572,8 @@ class DeviceAttention(_Resident):
 
     def forward(self, x, pos, slots, pages, q_start, kv_len, add=None, out=None, stream=None):
         """[T, H]: attention of the rows x [T, H] (bf16, normed), whose keys and values go to the cache first, through
-        the output projection, plus ``add`` [T, H].  Rows outside all sequences of q_start are projections of whatever
-        the workspace held."""
+        the output projection, plus ``add`` [T, H].  Rows outside all sequences of q_start hold nothing of use, but
+        nothing of others either, and are finite where x is."""
         import torch
         T, bf = x.shape[0], (torch.bfloat16,)
         rows = ((T, self.H),)
@@ -587,10 +588,11 @@ class DeviceAttention(_Resident):
         self._note_stream(stream)
         w = self.w
         moe.moe_gemm(x, w["w_qkv"], self.b["b_qkv"], None, T, qkv.shape[1], self.H, qkv, stream=stream)
-        moe.moe_cache_write(q, w["q_norm"], q, k, w["k_norm"], v, pos if self.rot else None, self.freq, slots, T, self.Hq,
-                            self.Hkv, self.D, self.rot, self.pairs, self.k_cache, self.v_cache, self.k_scale,
+        # rows of no sequence keep their q, so that what follows on the stream takes finite rows alone
+        moe.moe_cache_write(q, w["q_norm"], o, k, w["k_norm"], v, pos if self.rot else None, self.freq, slots, T,
+                            self.Hq, self.Hkv, self.D, self.rot, self.pairs, self.k_cache, self.v_cache, self.k_scale,
                             self.v_scale, self.n_pages, self.page, self.mscale, self.w_add, self.eps, stream)
-        moe.moe_attention(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, pages, q_start, kv_len, T, S,
+        moe.moe_attention(o, self.k_cache, self.v_cache, self.k_scale, self.v_scale, pages, q_start, kv_len, T, S,
                           self.Hq, self.Hkv, self.D, self.n_pages, self.page, m, o, part, self.scale, self.window,
                           stream=stream)
         moe.moe_gemm(o, w["w_o"], self.b["b_o"], add, T, self.H, self.Hq * self.D, out, stream=stream)

@@ -600,7 +600,7 @@ def moe_attention_workspace_size(T: int, S: int, Hq: int, Hkv: int, D: int, max_
 
 def moe_attention(q, k_cache, v_cache, k_scale, v_scale, pages, q_start, kv_len, T, S, Hq, Hkv, D, n_pages, P,
                   max_pages, out, workspace, scale: Optional[float] = None, window: int = 0, lse=None, stream=None):
-    """The type of k_cache is the cache's; q and out may be columns of wider rows.  workspace: a tensor of
+    """The type of k_cache is the cache's; q and out may be columns of wider rows, out may be q.  workspace: a tensor of
     moe_attention_workspace_size bytes or more, None where that is 0.  scale: None for D ** -0.5."""
     import torch
     q, q_ld = _rows("q", q, T, Hq * D)

@@ -103,6 +103,11 @@ def test_attention_refusals(L, kw, want):
     assert call(L.moe_attention, ATTEND, kw) == status(want)
 
 
+def test_attention_in_place_refusal(L):
+    assert call(L.moe_attention, ATTEND, dict(out_ld=520)) == moe.MOE_ERR_SHAPE
+    assert "in place" in moe.last_error()
+
+
 def test_attention_workspace(L):
     """What the query says is enough and one byte less is refused; sizes out of range need nothing."""
     size = moe.moe_attention_workspace_size

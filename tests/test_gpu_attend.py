@@ -386,6 +386,27 @@ def test_attention_rows_in_place_of_columns(torch):
     assert bool((to[:, :8] == -9.5).all()) and bool((to[:, 8 + c.Hq * c.D:] == -9.5).all())
 
 
+@pytest.mark.parametrize("lengths,D,kind", [([(1, 900), (0, 5), (3, 3)], 128, "bf16"),
+                                            ([(1, 5000)], 256, "bf16"),
+                                            ([(7, 40), (2, 0)], 64, "i8"),
+                                            ([(150, 400), (33, 20)], 128, "e4m3"),
+                                            ([(200, 4500)], 64, "bf16"),
+                                            ([(17000, 17000)], 128, "bf16")])
+def test_attention_in_place(torch, lengths, D, kind):
+    """out may be q: single tokens, shared-out keys, all row tiles; one sequence's row with an infinity in its q takes
+    the second pass over its keys."""
+    c = Case(torch, lengths, 8, 2, D, 16, kind, seed=11)
+    if c.S == 1 and c.T < 9000:
+        c.q[0, 3] = float("inf")
+    want, wl = c.run()
+    x = c.q.clone()
+    out, lse = c.run(q=x, out=x)
+    end = int(c.q_start[-1])
+    assert torch.equal(x[:end].view(torch.int16), want[:end].view(torch.int16))
+    assert torch.equal(lse.view(torch.int32), wl.view(torch.int32))
+    assert torch.equal(x[end:], c.q[end:])
+
+
 @pytest.mark.parametrize("lengths,where", [([(40, 40)], 20), ([(1, 300), (2, 300)], 299), ([(200, 700)], 650),
                                            ([(3, 9000)], 8998)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])

@@ -177,6 +177,32 @@ def test_blocks_on_a_residual_stream(torch, i8):
     assert rel(y1, y[10:].double()) < 0.05  # tiles and experts' loads differ, and a near tie may choose another expert
 
 
+def test_padded_batch(torch):
+    """Rows of no sequence are finite and their own, whatever the workspace held, so that the experts may follow; the
+    other rows are as without them."""
+    wl = synth.Workload("block", T=16, H=H, E=8, k=2, I=128, I_s=128, bias="normal")
+    layer = DeviceLayer.from_inputs(synth.make_inputs(wl, seed=1))
+    att, plain = attention(torch, "i8", seed=5), attention(torch, "i8", seed=5)
+    one = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    g = B.gen(33)
+    r0 = torch.randn(8, H, generator=g, device="cuda")
+    book = Book(torch, 3, 4, att.n_pages)
+    pos, slots, table, start, lens = book.step([1, 1, 1])
+    pad = torch.full((5,), -1, dtype=torch.int32, device="cuda")
+    got = []
+    for fill in (0, 255):  # 255: NaN in every type
+        att.forward(r0.to(torch.bfloat16), torch.cat([pos, pad]), torch.cat([slots, pad]), table, start, lens)
+        att._ws.fill_(fill)
+        r = r0.clone()
+        y = att.forward_block(r, None, one, torch.cat([pos, pad]), torch.cat([slots, pad]), table, start, lens)
+        z = layer.forward_block(r, y, one)
+        assert bool(y.isfinite().all()) and bool(z.isfinite().all()) and bool(r.isfinite().all())
+        got.append(y)
+    assert torch.equal(*got)
+    want = plain.forward_block(r0[:3].clone(), None, one, pos, slots, table, start, lens)
+    assert rel(got[0][:3], want.double()) < BOUND["i8"]
+
+
 def test_captured_steps_and_streams(torch):
     """A decode step captured once and replayed over a growing context, eager steps of another size between; the same
     on a stream of its own, whose pool holds what it allocates."""
