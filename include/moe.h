@@ -567,7 +567,7 @@ int moe_rope(const uint16_t* x, int64_t x_ld, const uint16_t* w_norm, float w_ad
  *   [0, n_pages * P) are padding and are not written; no two tokens name one slot.
  *   k_cache, v_cache [n_pages, Hkv, P, D] of `type`; k_scale, v_scale [n_pages, Hkv, P] fp32 for 8-bit types, else
  *   NULL.  A token's head is stored rounded to bf16, or as codes:  scale = max(max |x|, 2^-100) / top,
- *   code = x / scale rounded to nearest (x times top / max in fp32).  A head with an infinity or a NaN gets scale NaN
+ *   code = x / scale rounded to nearest (x * top / max in fp32).  A head with an infinity or a NaN gets scale NaN
  *   and codes 0.
  *   P a power of two, 16 <= P <= 1024; n_pages * P <= 2^30; Hq, Hkv <= 1024; the rest as moe_rope.
  */

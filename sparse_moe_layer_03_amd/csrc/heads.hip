@@ -12,7 +12,8 @@
 // position of 10^6 would leave the angle of the fastest pair 0.06 rad off), its sine and cosine in 32.
 //
 // Quantisation of a row as in moe_quantize_i8: a = max(max |x|, 2^-100), scale = a / top, code = x / scale rounded to
-// nearest, top = 127 or 448, as x times top / a in fp32; a row that holds Inf or NaN gets scale NaN and codes 0.
+// nearest, top = 127 or 448, as x times top / a in fp32, rounded once; a row that holds Inf or NaN gets scale NaN and
+// codes 0.
 #include "attend_internal.h"
 
 namespace moe {
@@ -220,18 +221,21 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs p, int per_tok
         const bool bad = m >= 0x7f800000u;
         constexpr float top = TYPE == MOE_I8 ? 127.0f : 448.0f;
         const float a = fmaxf(__uint_as_float(m), kQuantTiny), scale = a * (1.0f / top);
-        // top / a in 32 bits: the scale's reciprocal (a's own is no normal number for the largest) and its residual.
-        // Quotients x / scale halfway between two codes, which rows of bf16 values have many of, are then found as such.
-        const float near = __builtin_amdgcn_rcpf(scale), inv = fmaf(fmaf(-near, a, top), near * (1.0f / top), near);
+        // top / a as inv + low, to twice 24 bits: by the scale's reciprocal (a's own is no normal number for the
+        // largest) and residuals.  Quotients halfway between two codes, which rows of bf16 values have many of, are
+        // then found as such: x * top / a is representable there, and code() rounds once.
+        const float near = __builtin_amdgcn_rcpf(scale), back = near * (1.0f / top);
+        const float inv = fmaf(fmaf(-near, a, top), back, near), low = fmaf(-inv, a, top) * back;
+        auto code = [&](float x) { return fmaf(x, inv, x * low); };
         u32x2 w = {0u, 0u};
         if constexpr (TYPE == MOE_I8) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e >> 2] |= ((uint32_t)__float2int_rn(f[e] * inv) & 0xffu) << (8 * (e & 3));
+          for (int e = 0; e < 8; ++e) w[e >> 2] |= ((uint32_t)__float2int_rn(code(f[e])) & 0xffu) << (8 * (e & 3));
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
-            w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
+            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(code(f[4 * h]), code(f[4 * h + 1]), 0, false);
+            w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(code(f[4 * h + 2]), code(f[4 * h + 3]), v, true);
           }
         }
         if (bad) w = u32x2{0u, 0u};

@@ -245,6 +245,28 @@ def test_cache_halves(torch, kind, j):
             assert torch.equal(got[:31], want) and torch.equal(got[31:62], -want) and float(got[63]) == top
 
 
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("D", [8, 64, 200])
+def test_cache_codes_of_bf16_rows(torch, kind, D):
+    """Codes of bf16 rows are x * top / max rounded to nearest, halves to even, all of them.  With x = X 2^p and max = M
+    2^q in integers below 2^8, a boundary between codes is an odd B below 2^8 times a power of two, and X top and M B, up
+    to a power of two, are integers below 2^17: they are equal, where the quotient is the boundary itself and fp32 holds
+    it, or differ by more than 2^-17 of either, a hundred times what a quotient in fp32 is off by."""
+    T, Hkv, P = 512, 4, 64
+    n = T // P
+    top = A.TOP[kind]
+    x = torch.randn(T, Hkv * D, generator=B.gen(D), device="cuda").to(torch.bfloat16)
+    kc, vc, ks, vs = new_cache(torch, kind, n, Hkv, P, D)
+    slots = torch.arange(T, device="cuda").int()
+    moe.moe_cache_write(None, None, None, x, None, x, None, None, slots, T, 0, Hkv, D, 0, 0, kc, vc, ks, vs, n, P)
+    x = x.view(T, Hkv, D).double()
+    want = x * top / x.abs().amax(-1, keepdim=True)
+    want = want.round() if kind == "i8" else want.float().to(torch.float8_e4m3fn).double()
+    for c in (kc, vc):
+        got = c.float().permute(0, 2, 1, 3).reshape(T, Hkv, D).double()
+        assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ attention
 class Case:
     """Sequences (new tokens, keys) over a cache of random pages; slots and table entries that no row sees hold
