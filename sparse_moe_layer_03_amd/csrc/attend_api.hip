@@ -261,13 +261,14 @@ int moe_attention(const uint16_t* q, int64_t q_ld, const void* k_cache, const vo
 namespace moe {
 
 size_t attention_workspace(int T, int S, int Hq, int Hkv, int D, int64_t max_keys) {
-  // the type only widens row tiles that are not shared out
-  const attn::Plan p = attn::plan_of(MOE_BF16, T, S, Hq, Hkv, D, max_keys);
+  // the type only widens row tiles that are not shared out, and with a window there are no more shares than without
+  const attn::Plan p = attn::plan_of(MOE_BF16, T, S, Hq, Hkv, D, max_keys, 0);
   return p.stream && p.grid > 1 ? p.grid * (sizeof(attn::Part) + (size_t)2 * p.rows * (D + 2) * sizeof(float)) : 0;
 }
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
-  const attn::Plan p = attn::plan_of(a.type, a.T, a.S, a.Hq, a.Hkv, a.D, (int64_t)a.max_pages << a.page_shift);
+  const int64_t max_keys = (int64_t)a.max_pages << a.page_shift;
+  const attn::Plan p = attn::plan_of(a.type, a.T, a.S, a.Hq, a.Hkv, a.D, max_keys, a.window);
   if (a.type == MOE_I8) return attn::run_i8(a, p, st);
   if (a.type == MOE_E4M3) return attn::run_e4m3(a, p, st);
   return attn::run_bf16(a, p, st);

@@ -429,6 +429,18 @@ def test_attention_in_place(torch, lengths, D, kind):
     assert torch.equal(x[end:], c.q[end:])
 
 
+@pytest.mark.parametrize("lengths,Hq,Hkv,D,kind,window", [
+    ([(431, 4000), (100, 2500)], 5, 1, 256, "bf16", 129),   # far windows, row tiles: not shared out
+    ([(8, 3000), (1, 900), (5, 12)], 8, 2, 128, "i8", 1),   # the like for few rows
+    ([(40, 5000), (3, 5000)], 4, 2, 64, "e4m3", 2500),      # a long window, shared out
+    ([(300, 1500)], 4, 1, 128, "bf16", 0), ([(130, 1000), (64, 900)], 2, 2, 256, "i8", 0),  # few row tiles: small shares
+    ([(900, 900)], 2, 1, 64, "e4m3", 0)])
+def test_attention_shares(torch, lengths, Hq, Hkv, D, kind, window):
+    """Both sides of the rule by which keys are shared out, over long tables of pages."""
+    c = Case(torch, lengths, Hq, Hkv, D, 16, kind, window, seed=4)
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("lengths,where", [([(40, 40)], 20), ([(1, 300), (2, 300)], 299), ([(200, 700)], 650),
                                            ([(3, 9000)], 8998)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
