@@ -753,6 +753,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         const int r_pos = __builtin_amdgcn_readlane(pos, rr), r_vis = __builtin_amdgcn_readlane(vis0, rr);
         const uint16_t* qp = p.q + (q.q0 + r_tok) * p.q_ld + (int64_t)r_head * D;
         float qv[E], ov[E], rm = kNegInf, rl = 0.0f;
+        bool lost = false;  // all of O is NaN: so it stays
 #pragma unroll
         for (int e = 0; e < E; ++e) qv[e] = bf16_to_f32(qp[lane + 64 * e]), ov[e] = 0.0f;
         for (int j = 0; j < nt; ++j) {
@@ -774,10 +775,11 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
             for (int e = 0; e < E; ++e) ov[e] = ov[e] * f + wv * cached<C::CT>(p.v_cache, at * D + lane + 64 * e);
           }
-          bool lost = true;  // all of it NaN: so it stays
+          lost = true;
 #pragma unroll
           for (int e = 0; e < E; ++e) lost = lost && ov[e] != ov[e];
-          if (__all(lost)) break;
+          lost = __all(lost);
+          if (lost) break;
         }
 #pragma unroll
         for (int d = 0; d < C::DB; ++d)
@@ -787,7 +789,8 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
             const float v = __shfl(ov[d >> 1], at & 63);
             if (ql == rr) o[d][e] = v;
           }
-        if (ql == rr) mx = rm, l = rl;
+        // (the values are no part of m and l: where the keys behind were left out, theirs are in the first ones)
+        if (ql == rr && !lost) mx = rm, l = rl;
       }
     }
 
