@@ -599,7 +599,8 @@ int moe_cache_read(const void* k_cache, const void* v_cache, const float* k_scal
  *   Keys that no row sees are not read into any sum, whatever their slots hold: entries of pages that hold visible
  *   keys must lie in [0, n_pages) (else the rows that see them are NaN), others may hold anything.  kv_len beyond
  *   max_pages * P counts as that; q_start is cut to [0, T].  All three are read on the device.
- *   An infinity or a NaN in a key or value reaches the rows that see it and no others.
+ *   An infinity or a NaN in a key or value reaches the rows that see it and no others.  A row whose scores are all
+ *   -infinity is NaN (0 / 0), its lse -infinity.
  *   Hq % Hkv == 0; D 64, 128 or 256; scale > 0; T <= 2^24; T * Hq <= 2^30; S * Hkv <= 2^22; max_pages * P <= 2^30.
  *   workspace: moe_attention_workspace_size bytes (0: none needed) for these T, S, heads and max_keys = max_pages * P,
  *   16-byte aligned; it need not be cleared.  Scores, sums and out are fp32 until out is rounded; the softmax weights

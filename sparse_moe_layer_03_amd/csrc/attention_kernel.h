@@ -227,8 +227,13 @@ struct Part {
   int rows;  // of the item
   int row0;  // its first, in the sequence's (token, head) rows
   int q0, h;
-  int none[3];
+  int pos0;  // position of the sequence's token 0
+  int none[2];
 };
+// A row's factor at the end: no key is seen, out 0; keys whose scores are all -infinity, 0 / 0.
+__device__ __forceinline__ float inverse(float sum, int pos) {
+  return sum > 0.0f || sum != sum ? 1.0f / sum : pos < 0 ? 0.0f : __builtin_nanf("");
+}
 template <class C>
 __device__ __forceinline__ float* slot_at(const AttentionArgs& p, int slot) {
   return p.partial + (size_t)gridDim.x * (sizeof(Part) / 4) + (size_t)slot * C::R * (C::D + 2);
@@ -799,7 +804,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     if (STREAM && unit_lo == 0 && !whole && threadIdx.x == 0) {
       const int64_t last = u + units - 1;  // the item's last unit
       reinterpret_cast<Part*>(p.partial)[blockIdx.x] = {(int)(last / share) - (int)blockIdx.x + 1,
-                                                        min(n_rows - r0, C::R), r0, q.q0, h, {0, 0, 0}};
+                                                        min(n_rows - r0, C::R), r0, q.q0, h, pos0, {0, 0}};
     }
     float* slot = STREAM ? slot_at<C>(p, 2 * blockIdx.x + (unit_lo == 0 ? 1 : 0)) : nullptr;
     const int srow = wr * 32 + ql;  // row in the tile
@@ -820,7 +825,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
             sl > 0.0f || sl != sl ? (sm + log2f(sl)) * 0.6931471805599453f : kNegInf;
     };
     if constexpr (WK == 1) {
-      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      const float inv = inverse(l, pos);
       if (wave_live || to_slot) {
 #pragma unroll
         for (int d = 0; d < C::DB; ++d)
@@ -851,7 +856,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
 #pragma unroll
         for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = o[d][e] * f;
       __syncthreads();
-      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const float inv = inverse(sum, pos);
       const int lane_at = anew(lane);
       constexpr int PER = C::DB * 4 / WK;  // groups of four registers a wave adds up
 #pragma unroll
@@ -962,7 +967,7 @@ __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] += v[i][e] * fi;
         }
-      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const float inv = inverse(sum, t.pos0 + (t.row0 + r) / p.G);
 #pragma unroll
       for (int e = 0; e < E; ++e) put(r, lane + 64 * e, o[e], inv);
       if (p.lse && lane == 0) put_lse(r, top, sum);
@@ -1000,7 +1005,7 @@ __global__ __launch_bounds__(256) void combine_kernel(AttentionArgs p) {
 #pragma unroll
     for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = v[e];
     __syncthreads();
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    const float inv = inverse(sum, t.pos0 + (t.row0 + r) / p.G);
     if (threadIdx.x < C::D) {
       const int d = threadIdx.x;
       put(r, d, (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]), inv);

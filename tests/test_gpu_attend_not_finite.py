@@ -61,3 +61,21 @@ def test_value_row_of_nan(torch, kind, lengths, D, where, window):
             c.v[page, 1, place] = 0
             c.vs[page, 1, place] = NAN
     check(torch, c, 2 if c.T * 2 <= 32 * c.S else 1)
+
+
+@pytest.mark.parametrize("lengths,D,window,keys", [
+    ([(40, 40), (33, 20)], 128, 0, 1),       # the first row sees one key; rows that see none beside it
+    ([(1, 1), (1, 90)], 64, 0, 1), ([(5, 200)], 256, 1, 200),  # few rows, with a window of one key
+    ([(2, 30000)], 128, 0, 30000), ([(100, 9000)], 64, 0, 9000),  # contexts shared out
+    ([(300, 300)], 64, 3, 150)])             # rows that see such keys alone, some of them, none
+def test_scores_of_minus_infinity_alone(torch, lengths, D, window, keys):
+    """The weights of a row whose scores are all -infinity are 0 / 0: out is NaN, lse -infinity.  Rows that see no key
+    are 0."""
+    c = Case(torch, lengths, 4, 2, D, 16, "bf16", window, seed=23, poison=False)
+    q = c.q.view(c.T, 4, D)
+    q[..., 7] = q[..., 7].abs() + 0.5
+    at = torch.arange(min(keys, lengths[0][1]), device="cuda")
+    c.k[c.pages[0].long()[at // c.P], :, at % c.P, 7] = -INF
+    out, lse = check(torch, c, 2 if c.T * 2 <= 32 * c.S else 1)
+    ref = reference(c, 1)[0]
+    assert bool(ref.isnan().any()) and bool(out[:ref.shape[0]].view(ref.shape)[ref.isnan()].isnan().all())
