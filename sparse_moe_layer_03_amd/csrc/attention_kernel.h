@@ -12,9 +12,9 @@
 // it goes in as a second bf16 term (2^-16).  l sums the unrounded values.
 //
 // A masked key has P = 0, which does not undo an Inf or NaN in its V: rows behind the range of keys that the tile's
-// rows can see are zeroed on the way into LDS; a key inside it that only some rows see (later tokens, the window's
-// edge) could still poison the others, which shows as a non-finite O.  Rows with one are computed again, key by key
-// over the visible ones alone, at the end.
+// rows can see are zeroed on the way into LDS, and in tiles with keys that only some rows see (later tokens, the
+// window's edge) the values that are no numbers are, too.  These, behind all tiles, go to the rows that see them as
+// they are: a weight is positive, and a sum with one holds an Inf or NaN whatever the weight and the rest.
 //
 // Three shapes.  Up to 32 rows a sequence (decoding, drafts): 32 rows, four waves that deal the keys out between them,
 // K straight into the operand registers; the cache's bytes bound it.  64 requests of up to 8192 keys (4 heads of 128 in
@@ -89,7 +89,8 @@ struct Cfg {
   // requests at D 256 134 us, 151 with q in registers)
   static constexpr bool QLDS = KREG && D == 256 && !QUANT;
   static constexpr int SUMS = WK * NB * STAGE, QS = SUMS + (WK > 1 ? WK * 64 * 4 : 0);  // offsets in LDS
-  static constexpr int LDS = QS + (QLDS ? 32 * KROW : 0);
+  static constexpr int ODD = QS + (QLDS ? 32 * KROW : 0);
+  static constexpr int LDS = ODD + (WR > 1 ? 16 : 0);
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
   static_assert(WK == 1 || WR == 1, "");
@@ -213,12 +214,28 @@ __device__ __forceinline__ void widen(u32x4 w, u32x4& lo, u32x4& hi) {
   lo = u32x4{o[0], o[1], o[2], o[3]}, hi = u32x4{o[4], o[5], o[6], o[7]};
 }
 
+// Four elements of a cached row.
 template <int CT>
-__device__ __forceinline__ float cached(const void* p, int64_t i) {
-  if constexpr (CT == MOE_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  if constexpr (CT == MOE_I8) return (float)static_cast<const int8_t*>(p)[i];
-  return __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p)[i], 0);
+__device__ __forceinline__ void cached4(const void* p, int64_t i, float* f) {
+  if constexpr (CT == MOE_BF16) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = bf16_to_f32((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = CT == MOE_I8 ? (float)((int)(w << (24 - 8 * e)) >> 24) : __builtin_amdgcn_cvt_f32_fp8(w >> (8 * e), 0);
+  }
 }
+// The top bits of the elements of w that are no numbers (codes of int8 always are).
+template <int CT>
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) {
+  if constexpr (CT == MOE_BF16) return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  if constexpr (CT == MOE_E4M3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return 0u;
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
 // Partial results in the workspace: a Part per workgroup, then slots of R rows of O (unscaled, fp32) and R pairs
 // (m, l).  Part w: the item that begins in workgroup w's share and ends behind it.
@@ -251,6 +268,14 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
   const int wr = wave % WR, wk = wave / WR;
 
   const lds_bytes group = smem + wk * C::NB * C::STAGE;
+
+  // Two words, for this item and the next: bits of tiles (tile_bit) that values were taken out of.
+  MOE_LDS unsigned* const odd_tiles = lds_as<unsigned>(smem + C::ODD);
+  int turn = 0;
+  if constexpr (WR > 1) {
+    if (threadIdx.x < 2) odd_tiles[threadIdx.x] = 0u;
+    __syncthreads();
+  }
 
   // ---- this workgroup's work
   int64_t u = 0, u_end = 1, before = 0, share = 1;
@@ -288,6 +313,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       h = (int)(item / tiles), m = (int)(item - (int64_t)h * tiles);
     }
     const bool whole = unit_lo == 0 && unit_hi == units;
+    if (WR > 1 && STREAM && threadIdx.x == 0) odd_tiles[turn ^ 1] = 0u;
     // ---- rows (what lanes derive from their number is not kept over the items: it would take some 40 registers)
     const int lane = anew(lane0), hh = lane >> 5, ql = lane & 31, gt = wr * 64 + lane;
     const int n_rows = q.n * p.G, r0 = m * C::R, wrow = r0 + wr * 32;
@@ -334,6 +360,20 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     auto key_of = [&](int j) { return base + ((u_first + j) * WK + wk) * KT; };
     const scalar_ptr pages = (scalar_ptr)(uintptr_t)(p.pages + (int64_t)s * p.max_pages);
     const int page_mask = (1 << p.page_shift) - 1;
+    // whether the workgroup's rows may differ in which of the tile's keys they see; such are among the first and the
+    // last sixteen (256 rows are 256 tokens at most)
+    auto mixed_tile = [&](int k0) {
+      return k0 + KT - 1 > pos0 + i_first || (p.window > 0 && k0 <= pos0 + i_last - p.window);
+    };
+    auto tile_bit = [&](int j) { return nt - 1 - j < 16 ? nt - 1 - j : 16 + j; };
+    unsigned odd = 0u;  // as odd_tiles, of a wave alone
+    auto taken_out = [&](int j) {
+      const unsigned bit = 1u << tile_bit(j);
+      if constexpr (KREG)
+        odd |= bit;
+      else if (lane == 0)
+        __hip_atomic_fetch_or(odd_tiles + turn, bit, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    };
     // the page of a key, or of the nearest key that the rows see
     auto page_of = [&](int key) { return pages[min(max(key, kb), ke - 1) >> p.page_shift]; };
 
@@ -435,6 +475,18 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           if (out || no_page) from[i] = u32x4{v, v, v, v};
         }
       }
+      if (C::CT != MOE_I8 && !is_k && mixed_tile(k0)) {
+        constexpr int TOP = C::QUANT ? 7 : 15;
+        uint32_t bits = 0u;
+#pragma unroll
+        for (int i = 0; i < C::NL; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b = odd_bits<C::CT>(from[i][e]);
+            bits |= b, from[i][e] &= ~(b | (b - (b >> TOP)));
+          }
+        if (__any(bits != 0u)) taken_out(j);
+      }
 #pragma unroll
       for (int i = 0; i < C::NL; ++i) {
         if (C::CHUNKS % C::GT != 0 && i * C::GT + wr * 64 >= C::CHUNKS) break;
@@ -462,7 +514,15 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       store_rows(rk, j, group + buf * C::STAGE, C::KROW, none, true);
     };
     auto store_v = [&](int j, int buf, unsigned none) { store_rows(rv, j, buf_v(buf), C::VROW, none, false); };
-    auto store_scales = [&](int buf) {
+    auto store_scales = [&](int j, int buf) {
+      if (mixed_tile(key_of(j))) {
+#pragma unroll
+        for (int i = 0; i < C::NS; ++i) {
+          const bool bad = i * C::GT + gt >= KT && !finite(rs[i]);
+          if (__any(bad)) taken_out(j);
+          if (bad) rs[i] = 0.0f;
+        }
+      }
       MOE_LDS float* ls = lds_as<float>(buf_v(buf) + KT * C::VROW);
 #pragma unroll
       for (int i = 0; i < C::NS; ++i) {
@@ -634,7 +694,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
         f32x16 x[C::KB] = {};
         scores_k(x);
         sync();  // the last tile's reads are done
-        if constexpr (C::QUANT) store_scales(0);
+        if constexpr (C::QUANT) store_scales(j, 0);
         store_v(j, 0, bad);
         if (j + 1 < nt) issue(j + 1);
         sync();
@@ -667,7 +727,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
       look_up(0);
       next_k(0), to_v(), next_v(0);
       store_k(0, 0, bad), store_v(0, 0, vbad);
-      if constexpr (C::QUANT) store_scales(0);
+      if constexpr (C::QUANT) store_scales(0, 0);
       if (nt > 1) {
         next_k(1);
         to_v(), next_v(1);
@@ -693,7 +753,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           if constexpr (!decltype(last)::value) {
             if (j + 2 < nt) store_k(j + 2, after, bad);
             store_v(j + 1, next, vbad);
-            if constexpr (C::QUANT) store_scales(next);
+            if constexpr (C::QUANT) store_scales(j + 1, next);
             if (j + 2 < nt) to_v(), next_v(j + 2);
             if (j + 3 < nt) next_k(j + 3);
           }
@@ -729,7 +789,7 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           if constexpr (!decltype(last)::value) {
             if (j + 2 < nt) store_k(j + 2, buf, bad);
             store_v(j + 1, buf ^ 1, vbad);
-            if constexpr (C::QUANT) store_scales(buf ^ 1);
+            if constexpr (C::QUANT) store_scales(j + 1, buf ^ 1);
             if (j + 2 < nt) to_v(), next_v(j + 2);
             if (j + 3 < nt) next_k(j + 3);
             sync();
@@ -741,61 +801,28 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
     }
     l = halves_sum(l);
 
-    // ---- rows whose O is not finite again, over their visible keys alone
-    {
-      bool fine = true;
-#pragma unroll
-      for (int d = 0; d < C::DB; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) fine = fine && fabsf(o[d][e]) < __builtin_inff();
-      const uint64_t b64 = __ballot(!fine);
-      unsigned rows = (unsigned)b64 | (unsigned)(b64 >> 32);
-      while (rows) {
-        const int rr = __ffs(rows) - 1;
-        rows &= rows - 1;
-        constexpr int E = D / 64;
-        const int r_tok = __builtin_amdgcn_readlane(tok, rr), r_head = __builtin_amdgcn_readlane(head, rr);
-        const int r_pos = __builtin_amdgcn_readlane(pos, rr), r_vis = __builtin_amdgcn_readlane(vis0, rr);
-        const uint16_t* qp = p.q + (q.q0 + r_tok) * p.q_ld + (int64_t)r_head * D;
-        float qv[E], ov[E], rm = kNegInf, rl = 0.0f;
-        bool lost = false;  // all of O is NaN: so it stays
-#pragma unroll
-        for (int e = 0; e < E; ++e) qv[e] = bf16_to_f32(qp[lane + 64 * e]), ov[e] = 0.0f;
-        for (int j = 0; j < nt; ++j) {
-          const int k0 = key_of(j);
-          for (int key = max(k0, r_vis); key < min(k0 + KT, r_pos + 1); ++key) {
-            const int page = page_of(key);
-            const bool none = (unsigned)page >= (unsigned)p.n_pages;
-            const int64_t at = (((int64_t)(none ? 0 : page) * p.Hkv + h) << p.page_shift) + (key & page_mask);
-            float d = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) d += qv[e] * cached<C::CT>(p.k_cache, at * D + lane + 64 * e);
-            d = wave_sum(d) * p.scale;
-            if (C::QUANT) d *= p.k_scale[at];
-            if (none) d = __builtin_nanf("");
-            const float to = fmaxf(rm, d), sub = to == kNegInf ? 0.0f : to;
-            const float f = exp2_fast(rm - sub), w = exp2_fast(d - sub);
-            rm = to, rl = rl * f + w;
-            const float wv = C::QUANT ? w * p.v_scale[at] : w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) ov[e] = ov[e] * f + wv * cached<C::CT>(p.v_cache, at * D + lane + 64 * e);
-          }
-          lost = true;
-#pragma unroll
-          for (int e = 0; e < E; ++e) lost = lost && ov[e] != ov[e];
-          lost = __all(lost);
-          if (lost) break;
-        }
+    // ---- what was taken out of mixed tiles, to the rows that see it (behind the barrier after the last store)
+    if constexpr (WR > 1) odd = __builtin_amdgcn_readfirstlane(odd_tiles[turn]), turn ^= 1;
+    while (odd != 0u) {
+      const int bit = __ffs(odd) - 1, k0 = key_of(bit < 16 ? nt - 1 - bit : bit - 16);
+      odd &= odd - 1u;
+#pragma unroll 1
+      for (int key = max(k0, kb); key < min(k0 + KT, ke); ++key) {
+        const int page = page_of(key);
+        if ((unsigned)page >= (unsigned)p.n_pages) continue;  // (the scores of its rows are NaN)
+        const int64_t at = (((int64_t)page * p.Hkv + h) << p.page_shift) + (key & page_mask);
+        const float f = C::QUANT ? p.v_scale[at] : 1.0f;
+        const bool seen = (unsigned)(key - vis0) < (unsigned)vis_n;
 #pragma unroll
         for (int d = 0; d < C::DB; ++d)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int at = 32 * d + 8 * (e >> 2) + 4 * hh + (e & 3);
-            const float v = __shfl(ov[d >> 1], at & 63);
-            if (ql == rr) o[d][e] = v;
+          for (int g = 0; g < 4; ++g) {
+            float v[4];
+            cached4<C::CT>(p.v_cache, at * D + 32 * d + 8 * g + 4 * hh, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (seen && !(finite(v[e]) && finite(f))) o[d][4 * g + e] += v[e] * f;
           }
-        // (the values are no part of m and l: where the keys behind were left out, theirs are in the first ones)
-        if (ql == rr && !lost) mx = rm, l = rl;
       }
     }
 

@@ -79,3 +79,92 @@ def test_scores_of_minus_infinity_alone(torch, lengths, D, window, keys):
     out, lse = check(torch, c, 2 if c.T * 2 <= 32 * c.S else 1)
     ref = reference(c, 1)[0]
     assert bool(ref.isnan().any()) and bool(out[:ref.shape[0]].view(ref.shape)[ref.isnan()].isnan().all())
+
+
+SPOTS = [
+    # lengths, heads, D, window, keys (as many as a sequence has are taken, some of them)
+    ([(40, 40), (1, 300), (0, 70)], 4, 2, 64, 0, (0, 5, 39, 290)),       # few rows
+    ([(9, 12000)], 2, 1, 128, 0, (3, 6001, 11993, 11999)),               # shared out
+    ([(7, 3000), (2, 500)], 8, 2, 256, 40, (470, 2960, 2975, 2999)),
+    ([(300, 900), (64, 64)], 4, 2, 64, 0, (7, 62, 601, 640, 899)),       # row tiles
+    ([(300, 900)], 4, 2, 128, 130, (480, 500, 600, 601, 897)),
+    ([(129, 700), (200, 200)], 2, 1, 256, 0, (11, 190, 580, 699)),
+    ([(180, 9000)], 4, 1, 64, 0, (100, 8821, 8990)),                     # row tiles shared out
+    ([(257, 257), (300, 431), (64, 64)] * 4, 64, 64, 128, 0, (0, 63, 64, 250, 420)),  # 256 rows a workgroup
+    ([(520, 600), (520, 520)] * 2, 64, 64, 128, 70, (0, 100, 111, 300, 519)),
+]
+
+
+@pytest.mark.parametrize("kind,bad", [("bf16", NAN), ("bf16", INF), ("bf16", -INF), ("i8", NAN), ("i8", INF),
+                                      ("e4m3", NAN), ("e4m3", "code")])
+@pytest.mark.parametrize("lengths,Hq,Hkv,D,window,keys", SPOTS)
+def test_values_that_are_no_numbers(torch, lengths, Hq, Hkv, D, window, keys, kind, bad):
+    """Single elements (a code or bf16 value) or rows (a scale) of some keys: early ones that all rows see, ones beside
+    the diagonal and the window's edge that some see.  What does not see them, or is another channel, keeps its bits."""
+    c = Case(torch, lengths, Hq, Hkv, D, 16, kind, window, seed=25, poison=False)
+    clean, cl = c.run()
+    for s, (n, L) in enumerate(lengths):
+        for i, key in enumerate(k for k in keys if k < L):
+            page, place = spot(c, s, key)
+            head, ch = (i + s) % Hkv, (17 * i + 5) % D
+            if kind == "bf16":
+                c.v[page, head, place, ch] = bad
+            elif bad == "code":
+                c.v.view(torch.uint8)[page, head, place, ch] = 0x7f + 0x80 * (i & 1)
+            else:
+                c.vs[page, head, place] = bad
+    out, lse = check(torch, c, 2 if c.T * (Hq // Hkv) <= 32 * c.S else 1)
+    lost = reference(c, 1)[0].isnan()
+    assert bool(lost.any())
+    got, was = (x[:lost.shape[0]].view(lost.shape) for x in (out, clean))
+    assert torch.equal(got[~lost].view(torch.int16), was[~lost].view(torch.int16))
+    assert torch.equal(lse, cl)
+
+
+def test_opposite_infinities(torch):
+    """Two infinities of opposite signs in a channel: rows that see one hold it, rows that see both are NaN."""
+    for lengths, Hq in (([(40, 300)], 1), ([(200, 200)], 4)):
+        c = Case(torch, lengths, Hq, 1, 64, 16, "bf16", seed=27, poison=False)
+        n, L = lengths[0]
+        a, b = L - 30, L - 12
+        for key, v in ((a, INF), (b, -INF)):
+            page, place = spot(c, 0, key)
+            c.v[page, 0, place, 9] = v
+        out, _ = c.run()
+        x = out[:n].view(n, Hq, 64)[..., 9].float()
+        pos = torch.arange(L - n, L, device="cuda")
+        assert bool(x[pos < a].isfinite().all()) and bool((x[(pos >= a) & (pos < b)] == INF).all())
+        assert bool(x[pos >= b].isnan().all())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8"])
+def test_they_cost_little(torch, kind):
+    """A prompt behind a token with a value that is no number is as fast as any, but for the tiles that some of the rows
+    see in part; with one in every key it stays within some ten times."""
+    c = Case(torch, [(4096, 4096)], 8, 1, 128, 64, kind, seed=29, poison=False)
+    ws = c.workspace()
+
+    def time():
+        best = float("inf")
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.run(workspace=ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    clean = time()
+    page, place = spot(c, 0, 3)
+    if kind == "bf16":
+        c.v[page, 0, place, 5] = NAN
+    else:
+        c.vs[page, 0, place] = NAN
+    early = time()
+    if kind == "bf16":
+        c.v[..., 5] = NAN
+    else:
+        c.vs.fill_(NAN)
+    every = time()
+    G.say(f"[not finite] {kind}: clean {clean * 1e3:.0f} us, an early key {early * 1e3:.0f}, every key {every * 1e3:.0f}")
+    assert early < 3 * clean and every < 10 * clean
