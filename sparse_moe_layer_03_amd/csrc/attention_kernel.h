@@ -94,6 +94,7 @@ struct Cfg {
   static constexpr int TERMS = WK > 1 ? 2 : 1;  // bf16 terms of P
   static constexpr int KB = KT / 32, NQ = D / 16, DB = D / 32;
   static_assert(WK == 1 || WR == 1, "");
+  static_assert(!TWO || !QUANT, "the two groups' steps store no scales");
   static_assert(WK == 1 || STAGE >= 32 * D * 4, "the waves' O are merged in their tiles");
   static_assert(LDS <= 160 * 1024, "");
 };
@@ -753,7 +754,6 @@ __device__ __forceinline__ void attention_body(const AttentionArgs& p, int min_u
           if constexpr (!decltype(last)::value) {
             if (j + 2 < nt) store_k(j + 2, after, bad);
             store_v(j + 1, next, vbad);
-            if constexpr (C::QUANT) store_scales(j + 1, next);
             if (j + 2 < nt) to_v(), next_v(j + 2);
             if (j + 3 < nt) next_k(j + 3);
           }
