@@ -1,0 +1,71 @@
+"""The rule that cuts an attention call into workgroups, compiled for the host."""
+import random
+import shutil
+import subprocess
+
+import pytest
+
+from sparse_moe_layer_03_amd import build
+
+MAIN = """
+#include <stdio.h>
+#include "attention_rule.h"
+int main() {
+  int type, T, S, Hq, Hkv, D, window;
+  long long keys;
+  while (scanf("%d %d %d %d %d %d %lld %d", &type, &T, &S, &Hq, &Hkv, &D, &keys, &window) == 8) {
+    const moe::attn::Plan p = moe::attn::plan_of(type, T, S, Hq, Hkv, D, keys, window);
+    printf("%d %d %d %d\\n", p.rows, (int)p.stream, p.grid, p.min_units);
+  }
+}
+"""
+BF16, I8, E4M3 = 0, 2, 3
+
+
+@pytest.fixture(scope="module")
+def rule(tmp_path_factory):
+    """rule([(type, T, S, Hq, Hkv, D, max_keys, window), ..]) -> [(rows, shared out, workgroups, least units), ..]"""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    d = tmp_path_factory.mktemp("rule")
+    (d / "main.cpp").write_text(MAIN)
+    exe = str(d / "rule")
+    subprocess.run([cxx, "-O1", "-std=c++17", "-Wall", "-Werror", "-I", build.CSRC, "-I", build.INCLUDE,
+                    str(d / "main.cpp"), "-o", exe], check=True)
+
+    def run(calls):
+        out = subprocess.run([exe], input="\n".join(" ".join(str(int(v)) for v in c) for c in calls), text=True,
+                             stdout=subprocess.PIPE, check=True).stdout
+        return [tuple(map(int, line.split())) for line in out.splitlines()]
+    return run
+
+
+def test_shapes(rule):
+    """Single tokens take 32 rows, prompts 128 or, where there are many of them, 256; long contexts are shared out."""
+    calls = [(BF16, 1, 1, 32, 4, 128, 128, 0), (BF16, 64, 64, 32, 4, 128, 8192, 0), (I8, 64, 64, 32, 4, 64, 8192, 0),
+             (BF16, 512, 1, 32, 4, 128, 512, 0), (BF16, 8192, 1, 32, 4, 128, 8192, 0), (I8, 8192, 1, 32, 4, 128, 8192, 0),
+             (BF16, 8192, 1, 32, 4, 64, 8192, 0), (BF16, 256, 1, 32, 4, 128, 33024, 0)]
+    want = [(32, 0), (32, 1), (32, 1), (128, 0), (256, 0), (128, 0), (128, 0), (128, 1)]
+    assert [(r, s) for r, s, _, _ in rule(calls)] == want
+
+
+def allowed(rng):
+    """A call within the entry point's limits, spread over their logarithms, the largest among them."""
+    Hkv = 1 << rng.randint(0, 6)
+    Hq = Hkv * rng.choice((1, 2, 3, 5, 8, 16))
+    T = max(1, min(int(2 ** rng.uniform(0, 24.01)), 1 << 24, (1 << 30) // Hq))
+    S = max(1, min(int(2 ** rng.uniform(0, 22.01)), (1 << 22) // Hkv))
+    if rng.random() < 0.3:
+        T, S = min(1 << 24, (1 << 30) // Hq), (1 << 22) // Hkv if rng.random() < 0.5 else S
+    return (rng.choice((BF16, I8, E4M3)), T, S, Hq, Hkv, rng.choice((64, 128, 256)),
+            max(16, int(2 ** rng.uniform(4, 30.01))), rng.choice((0, 0, int(2 ** rng.uniform(0, 30)))))
+
+
+def test_workspace_holds_every_plan(rule):
+    """The query knows neither type nor window: what a call shares out is no more than without them, in the same rows."""
+    rng = random.Random(3)
+    calls = [allowed(rng) for _ in range(6000)]
+    for c, (rows, stream, grid, _), most in zip(calls, rule(calls), rule([(BF16, *c[1:-1], 0) for c in calls])):
+        if stream and grid > 1:
+            assert most[0] == rows and most[1] and most[2] >= grid, (c, most)
