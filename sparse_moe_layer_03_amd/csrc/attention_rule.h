@@ -22,7 +22,9 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
   Plan p;
   const bool few = T * G <= 32 * (int64_t)S;
   auto items_of = [&](int rows) { return (T * G + rows - 1) / rows * Hkv; };
-  p.rows = few ? 32 : D == 128 && type == MOE_BF16 && items_of(256) >= 512 ? 256 : 128;
+  // a launch holds fewer than 2^32 threads, 512 each in workgroups of 256 rows (256 in the others: always)
+  const bool wide = D == 128 && type == MOE_BF16 && items_of(256) >= 512 && (T * G / 256 + S) * Hkv < 1 << 23;
+  p.rows = few ? 32 : wide ? 256 : 128;
   const int unit = few ? (D == 64 ? 256 : 128) : 64;
   const int64_t tiles = T * G / p.rows + S;  // or fewer
   const int64_t units = (max_keys + 63 + unit - 1) / unit;

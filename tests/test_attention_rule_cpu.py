@@ -69,3 +69,13 @@ def test_workspace_holds_every_plan(rule):
     for c, (rows, stream, grid, _), most in zip(calls, rule(calls), rule([(BF16, *c[1:-1], 0) for c in calls])):
         if stream and grid > 1:
             assert most[0] == rows and most[1] and most[2] >= grid, (c, most)
+
+
+def test_launches_hold_their_threads(rule):
+    """A launch holds fewer than 2^32 threads per grid dimension."""
+    rng = random.Random(4)
+    calls = [allowed(rng) for _ in range(6000)]
+    calls += [(BF16, (1 << 30) // Hq, (1 << 22) // Hkv, Hq, Hkv, 128, 1024, 0)
+              for Hq, Hkv in ((64, 1), (64, 64), (128, 8), (1024, 1024), (1024, 1))]
+    for c, (rows, _, grid, _) in zip(calls, rule(calls)):
+        assert 0 < grid * (512 if rows == 256 else 256) < 1 << 32, (c, rows, grid)
