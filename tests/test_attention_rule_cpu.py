@@ -6,6 +6,8 @@ import subprocess
 import pytest
 
 from sparse_moe_layer_03_amd import build
+from tests import test_gpu_attend_not_finite as not_finite
+from tests import test_gpu_attend_wide as wide
 
 MAIN = """
 #include <stdio.h>
@@ -79,3 +81,15 @@ def test_launches_hold_their_threads(rule):
               for Hq, Hkv in ((64, 1), (64, 64), (128, 8), (1024, 1024), (1024, 1))]
     for c, (rows, _, grid, _) in zip(calls, rule(calls)):
         assert 0 < grid * (512 if rows == 256 else 256) < 1 << 32, (c, rows, grid)
+
+
+def test_shape_of_the_wide_cases(rule):
+    """What the GPU tests take for workgroups of 256 rows is cut so."""
+    calls = []
+    for lengths, Hq, Hkv, P, window in wide.CASES:
+        T = sum(n for n, _ in lengths) + wide.SPARE
+        keys = (max(-(-L // P) for _, L in lengths) + 2) * P
+        calls.append((BF16, T, len(lengths), Hq, Hkv, wide.D, keys, window))
+    for lengths, Hq, Hkv, D, window, _ in not_finite.SPOTS[-2:]:
+        calls.append((BF16, sum(n for n, _ in lengths) + 3, len(lengths), Hq, Hkv, D, 1024, window))
+    assert [r for r, *_ in rule(calls)] == [256] * len(calls)
