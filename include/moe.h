@@ -531,7 +531,8 @@ int moe_grouped_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* b, 
  *   MOE_ROPE_LINEAR  the same over `factor`: positions interpolated
  *   MOE_ROPE_NTK     base replaced by base * factor^(rot / (rot - 2))
  *   MOE_ROPE_YARN    pairs that turn more than 32 times within `original` tokens as plain, those that turn less than
- *                    once as linear, a linear ramp over the pairs between; mscale = 0.1 ln(factor) + 1
+ *                    once as linear, a linear ramp (in the pair's index, between whole pairs) over those between;
+ *                    mscale = 0.1 ln(factor) + 1
  * *mscale is 1 otherwise.  base > 1; factor >= 1 where used; original >= 1 where used.
  */
 #define MOE_ROPE_PLAIN 0

@@ -105,7 +105,8 @@ int moe_rope_frequencies(int rot, double base, int scaling, double factor, doubl
     double v = pow(b, -2.0 * i / rot) / two_pi;
     if (scaling == MOE_ROPE_LINEAR) v /= factor;
     if (scaling == MOE_ROPE_YARN) {
-      const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+      // (at1 < 0: not even pair 0 turns once)
+      const double ramp = at1 < 0.0 ? 1.0 : fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
       v = v * (1.0 - ramp) + v / factor * ramp;
     }
     freq[i] = v;
