@@ -515,6 +515,9 @@ class DeviceAttention(_Resident):
         self.b = {key: None if weights.get(key) is None else
                   torch.from_numpy(np.ascontiguousarray(weights[key], np.float32)).to(self.device)
                   for key in ("b_qkv", "b_o")}
+        for key in ("w_qkv", "w_o"):
+            if self.w[key] is None:
+                raise ValueError(f"{key} is missing")
         H = self.w["w_qkv"].shape[1]
         for key, t, shape in (("w_qkv", self.w["w_qkv"], ((Hq + 2 * Hkv) * D, H)), ("w_o", self.w["w_o"], (H, Hq * D)),
                               ("q_norm", self.w["q_norm"], (D,)), ("k_norm", self.w["k_norm"], (D,)),
@@ -523,9 +526,12 @@ class DeviceAttention(_Resident):
                 raise ValueError(f"{key} has shape {tuple(t.shape)}; expected {shape}")
         self.H, self.Hq, self.Hkv, self.D = H, Hq, Hkv, D
         self.n_pages, self.page, self.window, self.scale = n_pages, page, window, scale
+        if freq is not None and (freq.dtype is not torch.float64 or freq.dim() != 1):
+            raise ValueError(f"freq is {freq.dtype} of shape {tuple(freq.shape)}; expected torch.float64 [rot / 2]")
         self.rot = 0 if freq is None else 2 * freq.numel()
         self.freq = None if freq is None else freq.to(self.device)
         self.mscale, self.pairs, self.w_add, self.eps = mscale, pairs, w_add, eps
+        self._check_sizes({"bf16": moe.BF16, "i8": moe.I8, "e4m3": moe.E4M3}[cache])
         dtype = {"bf16": torch.bfloat16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}[cache]
         shape = (n_pages, Hkv, page, D)
         self.k_cache, self.v_cache = (torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
@@ -543,6 +549,20 @@ class DeviceAttention(_Resident):
     @property
     def _width(self):
         return self.H
+
+    def _check_sizes(self, cache: int):
+        """The library's own checks of a step's sizes, by calls without rows: what a step would refuse behind work that
+        is enqueued already is refused here."""
+        L, H, Hq, Hkv, D = moe.lib(), self.H, self.Hq, self.Hkv, self.D
+        q, kv, none = Hq * D, Hkv * D, None
+        moe._check(L.moe_attention(none, q, none, none, none, none, cache, none, none, none, 0, 0, Hq, Hkv, D,
+                                   self.n_pages, self.page, 1, D ** -0.5 if self.scale is None else self.scale,
+                                   self.window, none, q, none, none, 0, none))
+        moe._check(L.moe_cache_write(none, q, none, none, q, none, kv, none, none, kv, self.w_add, self.eps, none, none,
+                                     self.mscale, none, 0, Hq, Hkv, D, self.rot, self.pairs, cache, self.n_pages,
+                                     self.page, none, none, none, none, none))
+        for N, K in ((q + 2 * kv, H), (H, q)):
+            moe._check(L.moe_gemm(none, none, none, moe.ACT_NONE, none, 0, N, K, none, moe.BF16, none))
 
     def _buffers(self, T: int, S: int, max_keys: int):
         """(q, k, v columns of one product's rows, rows of rotated q and then of attention's output, its workspace), views
