@@ -208,8 +208,12 @@ static int check_attention(const char* f, int T, int S, int Hq, int Hkv, int D) 
 }
 
 size_t moe_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, int64_t max_keys) {
-  if (check_attention("moe_attention_workspace_size", T, S, Hq, Hkv, D) || max_keys < 0 || max_keys > kMaxTokens)
+  const char* f = "moe_attention_workspace_size";
+  if (check_attention(f, T, S, Hq, Hkv, D)) return 0;
+  if (max_keys < 0 || max_keys > kMaxTokens) {
+    fail(MOE_ERR_SHAPE, "%s: max_keys=%lld outside [0, 2^30]", f, (long long)max_keys);
     return 0;
+  }
   ok();
   return T == 0 || S == 0 ? 0 : attention_workspace(T, S, Hq, Hkv, D, max_keys);
 }

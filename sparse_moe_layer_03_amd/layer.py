@@ -564,12 +564,11 @@ class DeviceAttention(_Resident):
         for N, K in ((q + 2 * kv, H), (H, q)):
             moe._check(L.moe_gemm(none, none, none, moe.ACT_NONE, none, 0, N, K, none, moe.BF16, none))
 
-    def _buffers(self, T: int, S: int, max_keys: int):
-        """(q, k, v columns of one product's rows, rows of rotated q and then of attention's output, its workspace), views
-        of the workspace."""
+    def _buffers(self, T: int, part: int):
+        """(q, k, v columns of one product's rows, rows of rotated q and then of attention's output, its workspace of
+        ``part`` bytes), views of the workspace."""
         import torch
         qkv, o = T * (self.Hq + 2 * self.Hkv) * self.D * 2, T * self.Hq * self.D * 2
-        part = moe.moe_attention_workspace_size(T, S, self.Hq, self.Hkv, self.D, max_keys)
         up = [-(-n // 256) * 256 for n in (qkv, o, part)]
         ws, _ = self._reserve(sum(up))
         rows = ws[:qkv].view(torch.bfloat16).view(T, -1)
@@ -579,16 +578,25 @@ class DeviceAttention(_Resident):
                 ws[up[0] + up[1]:up[0] + up[1] + part] if part else None)
 
     def _check_step(self, T, pos, slots, pages, q_start, kv_len):
+        """(S, columns of pages, bytes of attention's workspace) of a step that its kernels take, all of them."""
         import torch
         i32 = (torch.int32,)
-        S = kv_len.shape[0] if kv_len.dim() == 1 else -1
-        m = pages.shape[-1]
-        given = [("slots", slots, ((T,),), i32), ("pages", pages, ((S, m),), i32), ("q_start", q_start, ((S + 1,),), i32),
-                 ("kv_len", kv_len, ((S,),), i32)]
+        given = {"slots": slots, "pages": pages, "q_start": q_start, "kv_len": kv_len}
         if self.rot or pos is not None:
-            given.append(("pos", pos, ((T,),), i32))
-        self._check_tensors(*given)
-        return S, m
+            given["pos"] = pos
+        for name, t in given.items():
+            if t is None:
+                raise ValueError(f"{name} is missing")
+        S = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        m = pages.shape[1] if pages.dim() == 2 else -1
+        shapes = {"pages": (S, m), "q_start": (S + 1,), "kv_len": (S,)}
+        self._check_tensors(*((name, t, (shapes.get(name, (T,)),), i32) for name, t in given.items()))
+        if m < 1:
+            raise ValueError("pages has no columns")
+        part = moe.moe_attention_workspace_size(T, S, self.Hq, self.Hkv, self.D, m * self.page)
+        if part == 0 and (why := moe.last_error()):
+            raise moe.MoEError(moe.MOE_ERR_SHAPE, why)
+        return S, m, part
 
     def forward(self, x, pos, slots, pages, q_start, kv_len, add=None, out=None, stream=None):
         """[T, H]: attention of the rows x [T, H] (bf16, normed), whose keys and values go to the cache first, through
@@ -598,13 +606,13 @@ class DeviceAttention(_Resident):
         T, bf = x.shape[0], (torch.bfloat16,)
         rows = ((T, self.H),)
         self._check_tensors(*((n, t, rows, bf) for n, t in (("x", x), ("add", add), ("out", out)) if t is not None))
-        S, m = self._check_step(T, pos, slots, pages, q_start, kv_len)
+        S, m, part = self._check_step(T, pos, slots, pages, q_start, kv_len)
         if out is None:
             out = self._output(T, stream)
         if T == 0:
             return out
         with self._pool(stream):
-            qkv, q, k, v, o, part = self._buffers(T, S, m * self.page)
+            qkv, q, k, v, o, ws = self._buffers(T, part)
         self._note_stream(stream)
         w = self.w
         moe.moe_gemm(x, w["w_qkv"], self.b["b_qkv"], None, T, qkv.shape[1], self.H, qkv, stream=stream)
@@ -613,7 +621,7 @@ class DeviceAttention(_Resident):
                             self.Hq, self.Hkv, self.D, self.rot, self.pairs, self.k_cache, self.v_cache, self.k_scale,
                             self.v_scale, self.n_pages, self.page, self.mscale, self.w_add, self.eps, stream)
         moe.moe_attention(o, self.k_cache, self.v_cache, self.k_scale, self.v_scale, pages, q_start, kv_len, T, S,
-                          self.Hq, self.Hkv, self.D, self.n_pages, self.page, m, o, part, self.scale, self.window,
+                          self.Hq, self.Hkv, self.D, self.n_pages, self.page, m, o, ws, self.scale, self.window,
                           stream=stream)
         moe.moe_gemm(o, w["w_o"], self.b["b_o"], add, T, self.H, self.Hq * self.D, out, stream=stream)
         return out

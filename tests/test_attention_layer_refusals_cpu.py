@@ -53,3 +53,68 @@ def test_built(no_gpu_needed, kw):
 def test_not_built(no_gpu_needed, kw, match):
     with pytest.raises((ValueError, moe.MoEError), match=match):
         build(**kw)
+
+
+I32 = torch.int32
+STEP = dict(pos=torch.zeros(6, dtype=I32), slots=torch.zeros(6, dtype=I32), pages=torch.zeros(2, 3, dtype=I32),
+            q_start=torch.zeros(3, dtype=I32), kv_len=torch.zeros(2, dtype=I32))
+
+
+class Enqueued(Exception):
+    """A call has passed all checks."""
+
+
+@pytest.fixture
+def att(no_gpu_needed, monkeypatch):
+    def enqueued(*a, **kw):
+        raise Enqueued
+    for name in ("moe_gemm", "moe_block_norm", "moe_cache_write", "moe_attention"):
+        monkeypatch.setattr(moe, name, enqueued)
+    monkeypatch.setattr(DeviceAttention, "_note_stream", lambda self, stream: None)
+    return build(freq=turns(D // 2))
+
+
+def calls(att, **kw):
+    """The two ways to a step."""
+    x, r, w = torch.zeros(6, H, dtype=BF), torch.zeros(6, H), torch.zeros(H, dtype=BF)
+    step = {**STEP, **kw}
+    return (lambda: att.forward(x, **step)), (lambda: att.forward_block(r, x, w, **step))
+
+
+def test_step_passes(att):
+    for call in calls(att) + calls(att, pages=torch.zeros(0, 3, dtype=I32), q_start=torch.zeros(1, dtype=I32),
+                                   kv_len=torch.zeros(0, dtype=I32)):
+        with pytest.raises(Enqueued):
+            call()
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(pos=None), "pos is missing"), (dict(slots=None), "slots is missing"), (dict(pages=None), "pages is missing"),
+    (dict(q_start=None), "q_start is missing"), (dict(kv_len=None), "kv_len is missing"),
+    (dict(pages=torch.zeros(2, 0, dtype=I32)), "pages has no columns"),
+    (dict(pages=torch.zeros(6, dtype=I32)), "pages has shape"), (dict(pages=torch.tensor(0, dtype=I32)), "pages has shape"),
+    (dict(kv_len=torch.tensor(2, dtype=I32)), "pages has shape|kv_len has shape"),
+    # 2^24 + 64 pages of 64 tokens a sequence; without memory of their own
+    (dict(pages=torch.zeros(1, 1, dtype=I32).expand(2, (1 << 24) + 64)), "pages"),
+])
+def test_step_refused(att, kw, match):
+    for call in calls(att, **kw):
+        with pytest.raises((ValueError, moe.MoEError), match=match):
+            call()
+
+
+def test_step_of_too_many(att, monkeypatch):
+    """What the size query refuses: sequences times key heads above 2^22, longer tables, more rows than it takes."""
+    monkeypatch.setattr(DeviceAttention, "_check_tensors", lambda self, *t: None)
+
+    class Like:
+        def __init__(self, *shape):
+            self.shape = shape
+
+        def dim(self):
+            return len(self.shape)
+    S = (1 << 21) + 1
+    for kw in (dict(kv_len=Like(S), pages=Like(S, 3)), dict(pages=Like(2, (1 << 24) + 1))):
+        for call in calls(att, **kw):
+            with pytest.raises(moe.MoEError):
+                call()
