@@ -604,8 +604,9 @@ int moe_cache_read(const void* k_cache, const void* v_cache, const float* k_scal
  *   -infinity is NaN (0 / 0), its lse -infinity.
  *   Hq % Hkv == 0; D 64, 128 or 256; scale > 0; T <= 2^24; T * Hq <= 2^30; S * Hkv <= 2^22; max_pages * P <= 2^30.
  *   workspace: moe_attention_workspace_size bytes (0: none needed) for these T, S, heads and max_keys = max_pages * P,
- *   16-byte aligned; it need not be cleared.  (The query is 0 for sizes out of range too, with moe_last_error set.)  Scores, sums and out are fp32 until out is rounded; the softmax weights
- *   are rounded to bf16 for their product with v (with T * (Hq / Hkv) <= 32 * S to a sum of two bf16 terms).
+ *   16-byte aligned; it need not be cleared.  (The query is 0 for sizes out of range too, with moe_last_error set.)
+ *   Scores, sums and out are fp32 until out is rounded; the softmax weights are rounded to bf16 for their product with
+ *   v (with T * (Hq / Hkv) <= 32 * S to a sum of two bf16 terms).
  */
 size_t moe_attention_workspace_size(int T, int S, int Hq, int Hkv, int D, int64_t max_keys);
 int moe_attention(const uint16_t* q, int64_t q_ld, const void* k_cache, const void* v_cache, const float* k_scale,

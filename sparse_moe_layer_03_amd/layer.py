@@ -535,8 +535,10 @@ class DeviceAttention(_Resident):
         dtype = {"bf16": torch.bfloat16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}[cache]
         shape = (n_pages, Hkv, page, D)
         self.k_cache, self.v_cache = (torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
-        self.k_scale, self.v_scale = ((None, None) if cache == "bf16" else
-                                      (torch.zeros(shape[:3], device=self.device) for _ in range(2)))
+        self.k_scale = self.v_scale = None
+        if cache != "bf16":
+            self.k_scale, self.v_scale = (torch.zeros(shape[:3], dtype=torch.float32, device=self.device)
+                                          for _ in range(2))
         self._init_workspace()
         with torch.cuda.device(self.device):
             # the first forward may run on any stream

@@ -118,3 +118,13 @@ def test_step_of_too_many(att, monkeypatch):
         for call in calls(att, **kw):
             with pytest.raises(moe.MoEError):
                 call()
+
+
+def test_scales_under_another_default_type(no_gpu_needed):
+    was = torch.get_default_dtype()
+    torch.set_default_dtype(BF)
+    try:
+        att = build(cache="i8")
+    finally:
+        torch.set_default_dtype(was)
+    assert att.k_scale.dtype is att.v_scale.dtype is torch.float32
