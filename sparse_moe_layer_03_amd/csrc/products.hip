@@ -190,10 +190,11 @@ __device__ __forceinline__ void store_block(const ProductArgs& p, const BlockRow
 // ---------------------------------------------------------------------------------------------------------------
 // Few rows (dense products): a workgroup owns 16 columns and reads their weights once, straight into
 // registers.  Its W waves take every W-th 128-byte line of the rows (two 16 x 16 matrix instructions deep), U lines at
-// a time, and add their partial sums through LDS.  The loads in flight bound it: an 8-bit row by 2048 x 4096 takes 3.2
-// us with four waves, a launch and one round of loads (the bytes alone would take 1.8).  A bf16 row's lines are twice
-// as many: by 2048 x 4096, with weights that lie in no cache, eight waves take 8.1 us and four 10.0, by 512 x 8192 12.4
-// and 16.1, by 8192 x 4096 17.4 and 17.1 (3.9 TB/s); 40 rows by 2048 x 512 5.2 and 4.6.
+// a time, and add their partial sums through LDS.  The loads in flight bound it (sizes as rows x K x columns): 1 x 2048
+// x 4096 in 8 bits takes 3.2 us with four waves, a launch and one round of loads (the bytes alone would take 1.8).  A
+// bf16 row's lines are twice as many: 1 x 4096 x 2048, with weights that lie in no cache, takes 8.1 us with eight waves
+// and 10.0 with four, 1 x 8192 x 512 12.4 and 16.1, 1 x 4096 x 8192 17.4 and 17.1 (3.9 TB/s); 40 x 512 x 2048 5.2 and
+// 4.6.
 
 template <bool I8, bool F32, int EPI, int MT, int U, int W>
 __global__ __launch_bounds__(64 * W) void skinny_kernel(ProductArgs p) {
@@ -693,9 +694,9 @@ hipError_t dense_launch(const ProductArgs& p, hipStream_t st) {
     skinny_kernel<I8, F32, EPI, 1, 4, W><<<blocks, 64 * W, 0, st>>>(p);
     return hipGetLastError();
   }
-  // bf16, 17 and 32 rows against the best tile, the weights from HBM: 2048 x 512 3.9 and 4.2 against 4.7 and 5.0,
-  // 2048 x 4096 12.1 and 14.7 against 16.3 and 17.2, 4096 x 2048 8.1 and 9.4 against 10.1 and 10.7; 5120 x 2048 12.4 and
-  // 15.5 against 10.3 and 10.8, 33 rows by 2048 x 4096 19.8 against 16.0
+  // bf16, 17 and 32 rows against the best tile, the weights from HBM (K x columns): 512 x 2048 3.9 and 4.2 against 4.7
+  // and 5.0, 4096 x 2048 12.1 and 14.7 against 16.3 and 17.2, 2048 x 4096 8.1 and 9.4 against 10.1 and 10.7; 2048 x 5120
+  // 12.4 and 15.5 against 10.3 and 10.8, 33 rows by 4096 x 2048 19.8 against 16.0
   if constexpr (!I8)
     if (p.P <= 32 && blocks <= 256) {
       skinny_kernel<I8, F32, EPI, 2, 2, W><<<blocks, 64 * W, 0, st>>>(p);
