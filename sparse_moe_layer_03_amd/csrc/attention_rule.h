@@ -20,6 +20,10 @@ inline Plan plan_of(int type, int T, int S, int Hq, int Hkv, int D, int64_t max_
   // a sequence's rows, T at most, see no more than this of its keys
   if (window > 0) max_keys = std::min(max_keys, (int64_t)window + T + 63);
   Plan p;
+  // An average over the sequences, empty ones too: their lengths are on the device, and a captured call serves any.
+  // Where they differ much it is no good guide, us: one prompt of 1024 among 256 slots, 32 heads over 4, 56 (31 by
+  // itself); a single token behind 131072 keys beside 62 short ones and 2048 prompt tokens, in a tile of 128 rows that is
+  // not shared out, 2503 (55 by itself; the others 78 together, 64 and 44 apart).
   const bool few = T * G <= 32 * (int64_t)S;
   auto items_of = [&](int rows) { return (T * G + rows - 1) / rows * Hkv; };
   // a launch holds fewer than 2^32 threads, 512 each in workgroups of 256 rows (256 in the others: always)

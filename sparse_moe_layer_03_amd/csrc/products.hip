@@ -695,8 +695,8 @@ hipError_t dense_launch(const ProductArgs& p, hipStream_t st) {
     return hipGetLastError();
   }
   // bf16, 17 and 32 rows against the best tile, the weights from HBM (K x columns): 512 x 2048 3.9 and 4.2 against 4.7
-  // and 5.0, 4096 x 2048 12.1 and 14.7 against 16.3 and 17.2, 2048 x 4096 8.1 and 9.4 against 10.1 and 10.7; 2048 x 5120
-  // 12.4 and 15.5 against 10.3 and 10.8, 33 rows by 4096 x 2048 19.8 against 16.0
+  // and 5.0, 4096 x 2048 12.1 and 14.7 against 16.3 and 17.2, 2048 x 4096 8.1 and 9.4 against 10.1 and 10.7; 2048 x
+  // 5120 12.4 and 15.5 against 10.3 and 10.8, 33 rows by 4096 x 2048 19.8 against 16.0
   if constexpr (!I8)
     if (p.P <= 32 && blocks <= 256) {
       skinny_kernel<I8, F32, EPI, 2, 2, W><<<blocks, 64 * W, 0, st>>>(p);
