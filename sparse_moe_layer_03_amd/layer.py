@@ -582,17 +582,17 @@ class DeviceAttention(_Resident):
     def _check_step(self, T, pos, slots, pages, q_start, kv_len):
         """(S, columns of pages, bytes of attention's workspace) of a step that its kernels take, all of them."""
         import torch
+        if slots is None or pages is None or q_start is None or kv_len is None or (pos is None and self.rot):
+            given = {"pos": pos if self.rot else 0, "slots": slots, "pages": pages, "q_start": q_start, "kv_len": kv_len}
+            raise ValueError(f"{next(name for name, t in given.items() if t is None)} is missing")
         i32 = (torch.int32,)
-        given = {"slots": slots, "pages": pages, "q_start": q_start, "kv_len": kv_len}
-        if self.rot or pos is not None:
-            given["pos"] = pos
-        for name, t in given.items():
-            if t is None:
-                raise ValueError(f"{name} is missing")
         S = kv_len.shape[0] if kv_len.dim() == 1 else -1
         m = pages.shape[1] if pages.dim() == 2 else -1
-        shapes = {"pages": (S, m), "q_start": (S + 1,), "kv_len": (S,)}
-        self._check_tensors(*((name, t, (shapes.get(name, (T,)),), i32) for name, t in given.items()))
+        given = [("slots", slots, ((T,),), i32), ("pages", pages, ((S, m),), i32), ("q_start", q_start, ((S + 1,),), i32),
+                 ("kv_len", kv_len, ((S,),), i32)]
+        if pos is not None:
+            given.append(("pos", pos, ((T,),), i32))
+        self._check_tensors(*given)
         if m < 1:
             raise ValueError("pages has no columns")
         part = moe.moe_attention_workspace_size(T, S, self.Hq, self.Hkv, self.D, m * self.page)
@@ -608,7 +608,12 @@ class DeviceAttention(_Resident):
         T, bf = x.shape[0], (torch.bfloat16,)
         rows = ((T, self.H),)
         self._check_tensors(*((n, t, rows, bf) for n, t in (("x", x), ("add", add), ("out", out)) if t is not None))
-        S, m, part = self._check_step(T, pos, slots, pages, q_start, kv_len)
+        sizes = self._check_step(T, pos, slots, pages, q_start, kv_len)
+        return self._attend(x, pos, slots, pages, q_start, kv_len, *sizes, add, out, stream)
+
+    def _attend(self, x, pos, slots, pages, q_start, kv_len, S, m, part, add, out, stream):
+        """The step, its tensors checked, with _check_step's sizes."""
+        T = x.shape[0]
         if out is None:
             out = self._output(T, stream)
         if T == 0:
@@ -640,8 +645,8 @@ class DeviceAttention(_Resident):
         given = (("r", r, rows, (bf, torch.float32)), ("y", y, rows, (bf,)), ("w_pre", w_pre, one, (bf,)),
                  ("w_post", w_post, one, (bf,)), ("gate", gate, one + rows, (bf,)), ("out", out, rows, (bf,)))
         self._check_tensors(*(g for g in given if g[1] is not None))
-        self._check_step(T, pos, slots, pages, q_start, kv_len)
+        sizes = self._check_step(T, pos, slots, pages, q_start, kv_len)
         with self._pool(stream):
             x = torch.empty((T, self.H), dtype=bf, device=self.device)
         moe.moe_block_norm(r, y, w_post, gate, w_pre, T, self.H, r, x, None, None, r_scale, y_scale, w_add, eps, stream)
-        return self.forward(x, pos, slots, pages, q_start, kv_len, out=out, stream=stream)
+        return self._attend(x, pos, slots, pages, q_start, kv_len, *sizes, None, out, stream)
